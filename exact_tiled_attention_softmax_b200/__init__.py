@@ -15,7 +15,8 @@ from dataclasses import dataclass
 import torch
 
 __all__ = [
-    "AllowedSet", "AttentionFunction", "AttnError", "attention", "attn_fwd", "attn_bwd", "attn_bwd_noalloc", "attn_fwd_workspace_size",
+    "AllowedSet", "AttentionFunction", "AttnError", "PagedCache", "attention", "attn_cache_read", "attn_cache_write",
+    "attn_paged_fwd", "attn_paged_workspace_size", "attn_fwd", "attn_bwd", "attn_bwd_noalloc", "attn_fwd_workspace_size",
     "attn_bwd_workspace_size", "attn_get_status", "attn_selftest_wait_timeout", "attn_set_kernel_events",
     "attn_status_string",
     "attn_version", "library_path", "load_library",
@@ -32,10 +33,13 @@ ATTN_DEVERR_TOPK_INDEX = 0x1
 ATTN_DEVERR_OVERFLOW = 0x2
 ATTN_DEVERR_TIMEOUT = 0x4
 ATTN_DEVERR_TOPK_CAUSAL = 0x8
+ATTN_DEVERR_PAGE = 0x10
+ATTN_DEVERR_RAGGED = 0x20
 
 ATTN_F32 = 0
 ATTN_BF16 = 1
 ATTN_F16 = 2
+ATTN_E4M3 = 3  # paged caches only
 
 ATTN_MASK_CAUSAL = 0x1
 ATTN_MASK_WINDOW = 0x2
@@ -44,6 +48,7 @@ ATTN_MASK_TOPK = 0x8
 ATTN_MASK_LENGTHS = 0x10
 ATTN_MASK_STARTS = 0x20
 ATTN_MASK_TOPK_CHECK_CAUSAL = 0x40
+ATTN_MASK_FIRST = 0x80
 ATTN_LSE_KV_ONLY = 0x1
 ATTN_LSE_NEG_LOG2 = 0x2
 ATTN_BWD_DETERMINISTIC = 0x1
@@ -70,7 +75,14 @@ class AttnMaskC(ctypes.Structure):
                 ("sink", ctypes.c_void_p), ("dropout_p", ctypes.c_float),
                 ("dropout_seed", ctypes.c_uint64), ("lengths", ctypes.c_void_p),
                 ("starts", ctypes.c_void_p), ("starts_stride_b", ctypes.c_int64),
-                ("lse_format", ctypes.c_uint32), ("bwd_flags", ctypes.c_uint32)]
+                ("lse_format", ctypes.c_uint32), ("bwd_flags", ctypes.c_uint32),
+                ("window_first", ctypes.c_int64)]
+
+
+class AttnCacheC(ctypes.Structure):
+    _fields_ = [("k", AttnTensorC), ("v", AttnTensorC), ("k_scale", AttnTensorC), ("v_scale", AttnTensorC),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32), ("seq_lens", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -100,6 +112,15 @@ def load_library():
     lib.attn_bwd.argtypes = [T, T, T, T, T, T, M, ctypes.c_float, T, T, T, vp, vp, sz, vp]
     lib.attn_bwd_noalloc.restype = ctypes.c_int
     lib.attn_bwd_noalloc.argtypes = [T, T, T, T, T, T, M, ctypes.c_float, T, T, T, vp, vp]
+    C = ctypes.POINTER(AttnCacheC)
+    lib.attn_cache_write.restype = ctypes.c_int
+    lib.attn_cache_write.argtypes = [T, T, vp, C, vp, sz, vp]
+    lib.attn_cache_read.restype = ctypes.c_int
+    lib.attn_cache_read.argtypes = [C, T, T, vp, sz, vp]
+    lib.attn_paged_workspace_size.restype = sz
+    lib.attn_paged_workspace_size.argtypes = [T, C, M]
+    lib.attn_paged_fwd.restype = ctypes.c_int
+    lib.attn_paged_fwd.argtypes = [T, vp, C, M, ctypes.c_float, ctypes.c_int32, T, T, vp, sz, vp]
     lib.attn_get_status.restype = ctypes.c_int
     lib.attn_get_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.attn_selftest_wait_timeout.restype = ctypes.c_int
@@ -124,15 +145,13 @@ def attn_version() -> int:
     return int(load_library().attn_version())
 
 
-_DTYPES = {torch.float32: ATTN_F32, torch.bfloat16: ATTN_BF16, torch.float16: ATTN_F16}
+_DTYPES = {torch.float32: ATTN_F32, torch.bfloat16: ATTN_BF16, torch.float16: ATTN_F16,
+           torch.float8_e4m3fn: ATTN_E4M3}
 
 
-def _tensor(t: torch.Tensor | None):
-    if t is None:
-        return None
+def _fill(c: AttnTensorC, t: torch.Tensor) -> AttnTensorC:
     if t.dim() > 4:
         raise ValueError("at most 4 dimensions")
-    c = AttnTensorC()
     c.data = t.data_ptr() if t.numel() else 0
     c.dtype = _DTYPES.get(t.dtype, -1)
     c.ndim = t.dim()
@@ -140,6 +159,10 @@ def _tensor(t: torch.Tensor | None):
         c.shape[i] = t.shape[i]
         c.stride[i] = t.stride(i)
     return c
+
+
+def _tensor(t: torch.Tensor | None):
+    return None if t is None else _fill(AttnTensorC(), t)
 
 
 def _ref(c):
@@ -178,6 +201,8 @@ class AllowedSet:
     lse_kv_only / lse_neg_log2 select the LSE format that attn_fwd writes
     and attn_bwd expects: the sink left out, and/or stored as -log2 Z.
     deterministic makes every gradient of attn_bwd bitwise reproducible.
+    window_first keeps the first keys visible outside the window (needs
+    window_left; not with starts).
     topk_check_causal turns on the debug check of the top-k lists against
     each token's causal position (ATTN_DEVERR_TOPK_CAUSAL in the status).
     """
@@ -198,6 +223,7 @@ class AllowedSet:
     lse_neg_log2: bool = False
     deterministic: bool = False
     topk_check_causal: bool = False
+    window_first: int = 0
 
     def tensors(self) -> list:
         """The device tensors the descriptor points at."""
@@ -223,6 +249,9 @@ class AllowedSet:
         if self.window_left:
             flags |= ATTN_MASK_WINDOW
             m.window_left = int(self.window_left)
+        if self.window_first:
+            flags |= ATTN_MASK_FIRST
+            m.window_first = int(self.window_first)
         if self.block_mask is not None:
             bm = self.block_mask
             flags |= ATTN_MASK_BLOCK
@@ -405,6 +434,165 @@ def attn_set_kernel_events(begin: "torch.cuda.Event | None", end: "torch.cuda.Ev
         if not ev.cuda_event:
             ev.record()
     load_library().attn_set_kernel_events(ctypes.c_void_p(begin.cuda_event), ctypes.c_void_p(end.cuda_event))
+
+
+@dataclass
+class PagedCache:
+    """A paged K/V cache (attn_cache) on one GPU.
+
+    k [num_pages, page_size, Hkv, d] and v [num_pages, page_size, Hkv, dv]
+    (float32, bfloat16, float16 or float8_e4m3fn; any stride order, the last
+    dimension contiguous), k_scale and v_scale float32 [num_pages, page_size,
+    Hkv] with an e4m3 pool. block_table int32 [batch, max_pages]: the pages of
+    each sequence, in order; seq_lens int32 [batch]: its cached positions, the
+    tokens of the step in hand included.
+    """
+    k: torch.Tensor
+    v: torch.Tensor
+    block_table: torch.Tensor
+    seq_lens: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+    @classmethod
+    def allocate(cls, num_pages: int, page_size: int, kv_heads: int, d: int, batch: int, max_pages: int, *,
+                 dv: int | None = None, dtype=torch.bfloat16, device="cuda") -> "PagedCache":
+        """An empty cache: zeroed pool (each head's rows of a page next to one
+        another, the order the attention kernels read), table and lengths."""
+        def pool(*inner, dtype):
+            return torch.zeros(num_pages, kv_heads, page_size, *inner, dtype=dtype, device=device).transpose(1, 2)
+
+        quant = dtype == torch.float8_e4m3fn
+        return cls(pool(d, dtype=dtype), pool(d if dv is None else dv, dtype=dtype),
+                   torch.zeros(batch, max_pages, dtype=torch.int32, device=device),
+                   torch.zeros(batch, dtype=torch.int32, device=device),
+                   pool(dtype=torch.float32) if quant else None, pool(dtype=torch.float32) if quant else None)
+
+    def tensors(self) -> list:
+        return [t for t in (self.k, self.v, self.block_table, self.seq_lens, self.k_scale, self.v_scale)
+                if t is not None]
+
+    def to_c(self) -> AttnCacheC:
+        """The C descriptor, after the checks that raw pointers cannot carry."""
+        _check_mask_tensor(self.block_table, "block_table", (torch.int32,), (2,))
+        _check_mask_tensor(self.seq_lens, "seq_lens", (torch.int32,), (1,))
+        if self.block_table.shape[0] != self.seq_lens.shape[0]:
+            raise ValueError("block_table and seq_lens hold different numbers of sequences")
+        _check_on(self.k.device, *self.tensors())
+        c = AttnCacheC()
+        _fill(c.k, self.k)
+        _fill(c.v, self.v)
+        if self.k_scale is not None:
+            _fill(c.k_scale, self.k_scale)
+        if self.v_scale is not None:
+            _fill(c.v_scale, self.v_scale)
+        c.batch, c.max_pages = self.block_table.shape
+        c.block_table, c.table_stride = self.block_table.data_ptr(), self.block_table.stride(0)
+        c.seq_lens = self.seq_lens.data_ptr()
+        return c
+
+
+def _cu_q_ptr(cu_q, cache: PagedCache):
+    if cu_q is None:
+        return None
+    _check_mask_tensor(cu_q, "cu_q", (torch.int32,), (1,))
+    if cu_q.shape[0] != cache.seq_lens.shape[0] + 1:
+        raise ValueError(f"cu_q holds {cu_q.shape[0]} entries, expected one more than the sequences")
+    _check_on(cache.k.device, cu_q)
+    return cu_q.data_ptr()
+
+
+def _launch_on(device: torch.device, call, stream) -> int:
+    """call(stream handle) with `device` current: the library launches on the
+    current device, and the default stream is that device's current one."""
+    if device.index == torch.cuda.current_device():
+        return call(_stream_handle(stream))
+    with torch.cuda.device(device):
+        return call(_stream_handle(stream))
+
+
+def _workspace_args(workspace) -> tuple:
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def attn_cache_write(k, v, cache: PagedCache, cu_q=None, *, workspace=None, stream=None) -> PagedCache:
+    """Write new tokens' rows k [rows, Hkv, d], v [rows, Hkv, dv] at the ends
+    of the cache's sequences (cu_q int32 [batch + 1]; None: the same number
+    each), quantised when the cache is e4m3. With a workspace of at least 256
+    bytes, attn_get_status reports bad pages and lengths. Returns the cache."""
+    ck, cv, c = _tensor(k), _tensor(v), cache.to_c()
+    cu = _cu_q_ptr(cu_q, cache)
+    _check_on(cache.k.device, k, v, workspace)
+    rc = _launch_on(k.device, lambda s: load_library().attn_cache_write(
+        _ref(ck), _ref(cv), cu, _ref(c), *_workspace_args(workspace), s), stream)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_write")
+    return cache
+
+
+def attn_cache_read(cache: PagedCache, max_len: int | None = None, *, dtype=None, k=None, v=None, workspace=None,
+                    stream=None):
+    """Read the cache back as dense (k [batch, Hkv, T, d], v [batch, Hkv, T,
+    dv]), T = max_len (default: all that the table can hold). Rows past a
+    sequence's length are left as they were in k and v given by the caller and
+    are zero in new ones. dtype (new tensors): default the pool's, bfloat16
+    for an e4m3 pool."""
+    if k is None or v is None:
+        P, page, H, d = cache.k.shape
+        T = int(max_len) if max_len is not None else cache.block_table.shape[1] * page
+        if dtype is None:
+            dtype = torch.bfloat16 if cache.k.dtype == torch.float8_e4m3fn else cache.k.dtype
+        B = cache.seq_lens.shape[0]
+        k = torch.zeros(B, H, T, d, dtype=dtype, device=cache.k.device) if k is None else k
+        v = torch.zeros(B, H, T, cache.v.shape[3], dtype=dtype, device=cache.k.device) if v is None else v
+    ck, cv, c = _tensor(k), _tensor(v), cache.to_c()
+    _check_on(cache.k.device, k, v, workspace)
+    rc = _launch_on(k.device, lambda s: load_library().attn_cache_read(
+        _ref(c), _ref(ck), _ref(cv), *_workspace_args(workspace), s), stream)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_read")
+    return k, v
+
+
+def attn_paged_workspace_size(q, cache: PagedCache, allowed: AllowedSet | None = None) -> int:
+    cq, c = _tensor(q), cache.to_c()
+    m = allowed.to_c() if allowed else None
+    with torch.cuda.device(q.device):
+        return int(load_library().attn_paged_workspace_size(_ref(cq), _ref(c), _ref(m)))
+
+
+def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None = None, scale: float | None = None, *,
+                   max_q: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of new tokens q [rows, Hq, d] over a paged cache that already
+    holds them: query i of a sequence's n new tokens sits at position
+    seq_len - n + i. allowed: causal, window_left, window_first, sink and the
+    LSE formats. max_q: the largest number of new tokens of a sequence, when
+    known (it only chooses between kernels). Returns (o [rows, Hq, dv], lse
+    [rows, Hq])."""
+    lib = load_library()
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if out is None:
+        out = torch.empty(*q.shape[:-1], cache.v.shape[-1], dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    m = allowed.to_c() if allowed else None
+    cq, co, cl, c = _tensor(q), _tensor(out), _tensor(lse), cache.to_c()
+    cu = _cu_q_ptr(cu_q, cache)
+    _check_on(cache.k.device, q, out, lse, workspace, *(allowed.tensors() if allowed else ()))
+
+    def call(s):
+        ws = workspace
+        if ws is None:  # from the launching stream's pool: freed here, reused there after the call
+            with torch.cuda.stream(stream):
+                ws = _workspace(lib.attn_paged_workspace_size(_ref(cq), _ref(c), _ref(m)), q.device)
+        return lib.attn_paged_fwd(_ref(cq), cu, _ref(c), _ref(m), ctypes.c_float(scale), int(max_q), _ref(co),
+                                  _ref(cl), *_workspace_args(ws), s)
+
+    rc = _launch_on(q.device, call, stream)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_paged_fwd")
+    return out, lse
 
 
 class AttentionFunction(torch.autograd.Function):

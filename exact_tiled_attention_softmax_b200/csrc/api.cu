@@ -6,6 +6,7 @@
 
 #include "common.cuh"
 #include "launchers.h"
+#include "paged.cuh"
 #include "sm100_dense.h"
 #include "sm100_topk.h"
 
@@ -48,10 +49,14 @@ uint32_t flags_of(const attn_mask* m) { return m ? m->flags : 0u; }
 attn_status check_mask(const attn_mask* m) {
   if (!m) return ATTN_OK;
   const uint32_t known = ATTN_MASK_CAUSAL | ATTN_MASK_WINDOW | ATTN_MASK_BLOCK | ATTN_MASK_TOPK |
-                         ATTN_MASK_LENGTHS | ATTN_MASK_STARTS | ATTN_MASK_TOPK_CHECK_CAUSAL;
+                         ATTN_MASK_LENGTHS | ATTN_MASK_STARTS | ATTN_MASK_TOPK_CHECK_CAUSAL | ATTN_MASK_FIRST;
   if (m->flags & ~known) return ATTN_ERR_INVALID_ARG;
   if ((m->flags & ATTN_MASK_TOPK_CHECK_CAUSAL) && !(m->flags & ATTN_MASK_TOPK)) return ATTN_ERR_INVALID_ARG;
   if ((m->flags & ATTN_MASK_WINDOW) && m->window_left < 1) return ATTN_ERR_INVALID_ARG;
+  if (m->flags & ATTN_MASK_FIRST) {
+    if (!(m->flags & ATTN_MASK_WINDOW) || m->window_first < 0) return ATTN_ERR_INVALID_ARG;
+    if (m->flags & ATTN_MASK_STARTS) return ATTN_ERR_UNSUPPORTED;
+  }
   if (m->flags & ATTN_MASK_BLOCK) {
     if (!m->block_mask || m->block_q < 1 || m->block_k < 1) return ATTN_ERR_INVALID_ARG;
     if (m->bm_stride_b < 0 || m->bm_stride_h < 0 || m->bm_stride_q < 0) return ATTN_ERR_INVALID_ARG;
@@ -80,6 +85,7 @@ MaskP mask_params(const attn_mask* m) {
   p.st_sb = m->starts_stride_b;
   p.lse_fmt = m->lse_format;
   p.window = m->window_left;
+  if (m->flags & ATTN_MASK_FIRST) p.first = m->window_first < 0x7fffffff ? m->window_first : 0x7fffffff;
   p.bm = m->block_mask;
   p.bq = m->block_q;
   p.bk = m->block_k;
@@ -177,6 +183,91 @@ size_t bwd_topk_bytes(const Topk& s, const attn_tensor* q, const attn_mask* m) {
     n += align_up(attn::sm100_topk_bwd_scratch_bytes(s.Tq, s.H, s.Dqk, s.Dv, m->topk_max), 256);
   return n + lse_copy_bytes(m, (size_t)s.Tq * s.H);
 }
+
+int elem_bytes(int32_t dt) { return dt == ATTN_F32 ? 4 : dt == ATTN_E4M3 ? 1 : 2; }
+
+// A tensor the caller hands over as [shape...] of dtype dt: ranks, strides
+// that do not alias elements, element alignment, a pointer when not empty.
+attn_status check_pool(const attn_tensor* t, int ndim, const int64_t* shape, bool inner) {
+  if (!same_shape(t, ndim, shape) || (inner && !inner_contiguous(t))) return ATTN_ERR_INVALID_ARG;
+  int64_t n = 1;
+  for (int i = 0; i < ndim; ++i) {
+    n *= shape[i] > 0 ? 1 : 0;
+    if (shape[i] > 1 && t->stride[i] < 1) return ATTN_ERR_INVALID_ARG;
+  }
+  if (n && !t->data) return ATTN_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(t->data) % elem_bytes(t->dtype) ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+}
+
+// The cache descriptor's host-side checks, and the kernels' form of it.
+attn_status check_cache(const attn_cache* c, CacheP& p) {
+  if (!c || c->k.ndim != 4 || c->v.ndim != 4 || !dims_fit_int(&c->k) || !dims_fit_int(&c->v))
+    return ATTN_ERR_INVALID_ARG;
+  const int32_t dt = c->k.dtype;
+  if ((!valid_dtype(dt) && dt != ATTN_E4M3) || c->v.dtype != dt) return ATTN_ERR_INVALID_ARG;
+  memset(&p, 0, sizeof(p));
+  p.num_pages = (int32_t)c->k.shape[0];
+  p.page_size = (int32_t)c->k.shape[1];
+  p.Hkv = (int32_t)c->k.shape[2];
+  p.d = (int32_t)c->k.shape[3];
+  p.dv = (int32_t)c->v.shape[3];
+  if (p.page_size < 1 || p.Hkv < 1 || p.d < 1 || p.dv < 1) return ATTN_ERR_INVALID_ARG;
+  if (p.d > 576 || p.dv > 576) return ATTN_ERR_UNSUPPORTED;
+  const int64_t ks[4] = {p.num_pages, p.page_size, p.Hkv, p.d}, vs[4] = {p.num_pages, p.page_size, p.Hkv, p.dv};
+  attn_status st;
+  if ((st = check_pool(&c->k, 4, ks, true)) != ATTN_OK || (st = check_pool(&c->v, 4, vs, true)) != ATTN_OK) return st;
+  if (dt == ATTN_E4M3) {
+    if (c->k_scale.dtype != ATTN_F32 || c->v_scale.dtype != ATTN_F32) return ATTN_ERR_INVALID_ARG;
+    if ((st = check_pool(&c->k_scale, 3, ks, false)) != ATTN_OK || (st = check_pool(&c->v_scale, 3, ks, false)) != ATTN_OK)
+      return st;
+    p.ks = static_cast<const float*>(c->k_scale.data);
+    p.vs = static_cast<const float*>(c->v_scale.data);
+  } else if (c->k_scale.data || c->v_scale.data) {
+    return ATTN_ERR_INVALID_ARG;
+  }
+  if (c->batch < 0 || c->max_pages < 0 || (c->batch > 1 && c->table_stride < c->max_pages)) return ATTN_ERR_INVALID_ARG;
+  if (c->batch && (!c->seq_lens || (c->max_pages && !c->block_table))) return ATTN_ERR_INVALID_ARG;
+  if ((int64_t)c->max_pages * p.page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  p.k = c->k.data;
+  p.v = c->v.data;
+  for (int i = 0; i < 3; ++i) {
+    p.sk[i] = c->k.stride[i];
+    p.sv[i] = c->v.stride[i];
+    p.sks[i] = p.ks ? c->k_scale.stride[i] : 0;
+    p.svs[i] = p.vs ? c->v_scale.stride[i] : 0;
+  }
+  p.table = c->block_table;
+  p.table_stride = c->table_stride;
+  p.max_pages = c->max_pages;
+  p.batch = c->batch;
+  p.lens = c->seq_lens;
+  p.dtype = dt;
+  return ATTN_OK;
+}
+
+// Rows of new tokens: every sequence's share must be whole when cu_q is NULL.
+attn_status check_rows(int64_t rows, const int32_t* cu_q, CacheP& p) {
+  if (!cu_q && (p.batch ? rows % p.batch : rows) != 0) return ATTN_ERR_INVALID_ARG;
+  p.cu_q = cu_q;
+  p.rows = (int32_t)rows;
+  return ATTN_OK;
+}
+
+// May data of dtype dt stand in front of this cache (the same type, or any of
+// the unquantised ones before an e4m3 cache)?
+bool matches_cache(int32_t dt, const CacheP& p) { return valid_dtype(dt) && (p.dtype == ATTN_E4M3 || dt == p.dtype); }
+
+// The optional workspace of the cache's copies: cleared status word, or none.
+attn_status optional_status(void* ws, size_t bytes, cudaStream_t cs, CacheP& p) {
+  p.status = nullptr;
+  if (!ws) return ATTN_OK;
+  const attn_status st = check_workspace(ws, bytes, kStatusBytes);
+  if (st != ATTN_OK) return st;
+  p.status = static_cast<uint32_t*>(ws);
+  return cudaMemsetAsync(ws, 0, kStatusBytes, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+constexpr int64_t kMaxRowWarps = 1LL << 33;  // one warp a row: the grid's limit at eight warps a block
 
 }  // namespace
 
@@ -533,6 +624,100 @@ attn_status attn_bwd(const attn_tensor* q, const attn_tensor* k, const attn_tens
   }
   if (e == cudaSuccess && want_dsink)
     e = launch_dsink(mask->sink, lsep, delta, s.B, s.Hq, s.Tq, sl[0], sl[1], sl[2], true, dsink, cs);
+  return cuda_status(e);
+}
+
+attn_status attn_cache_write(const attn_tensor* k, const attn_tensor* v, const int32_t* cu_q, const attn_cache* cache,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  CacheP p;
+  attn_status st = check_cache(cache, p);
+  if (st != ATTN_OK) return st;
+  if (!k || !v || k->ndim != 3 || v->ndim != 3 || !dims_fit_int(k)) return ATTN_ERR_INVALID_ARG;
+  if (!matches_cache(k->dtype, p) || v->dtype != k->dtype) return ATTN_ERR_INVALID_ARG;
+  const int64_t rows = k->shape[0];
+  const int64_t ks[3] = {rows, p.Hkv, p.d}, vs[3] = {rows, p.Hkv, p.dv};
+  if (!same_shape(k, 3, ks) || !same_shape(v, 3, vs) || !inner_contiguous(k) || !inner_contiguous(v))
+    return ATTN_ERR_INVALID_ARG;
+  if (rows && (!k->data || !v->data)) return ATTN_ERR_INVALID_ARG;
+  if ((st = check_rows(rows, cu_q, p)) != ATTN_OK) return st;
+  if (rows * p.Hkv >= kMaxRowWarps) return ATTN_ERR_UNSUPPORTED;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if ((st = optional_status(workspace, workspace_bytes, cs, p)) != ATTN_OK) return st;
+  if (!rows || !p.batch) return ATTN_OK;
+  const int64_t snk[2] = {k->stride[0], k->stride[1]}, snv[2] = {v->stride[0], v->stride[1]};
+  return cuda_status(launch_cache_write(p, k->data, snk, v->data, snv, k->dtype, cs));
+}
+
+attn_status attn_cache_read(const attn_cache* cache, attn_tensor* k, attn_tensor* v, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  CacheP p;
+  attn_status st = check_cache(cache, p);
+  if (st != ATTN_OK) return st;
+  if (!k || !v || k->ndim != 4 || v->ndim != 4 || !dims_fit_int(k)) return ATTN_ERR_INVALID_ARG;
+  if (!matches_cache(k->dtype, p) || v->dtype != k->dtype) return ATTN_ERR_INVALID_ARG;
+  const int64_t T = k->shape[2];
+  const int64_t ks[4] = {p.batch, p.Hkv, T, p.d}, vs[4] = {p.batch, p.Hkv, T, p.dv};
+  if ((st = check_pool(k, 4, ks, true)) != ATTN_OK || (st = check_pool(v, 4, vs, true)) != ATTN_OK) return st;
+  if ((int64_t)p.batch * p.Hkv >= kMaxRowWarps / (T ? T : 1)) return ATTN_ERR_UNSUPPORTED;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if ((st = optional_status(workspace, workspace_bytes, cs, p)) != ATTN_OK) return st;
+  if (!p.batch || !T) return ATTN_OK;
+  const int64_t sok[3] = {k->stride[0], k->stride[1], k->stride[2]}, sov[3] = {v->stride[0], v->stride[1], v->stride[2]};
+  return cuda_status(launch_cache_read(p, k->data, sok, v->data, sov, (int)T, k->dtype, cs));
+}
+
+size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, const attn_mask* mask) {
+  (void)q;
+  (void)cache;
+  (void)mask;
+  return kStatusBytes;
+}
+
+attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn_cache* cache, const attn_mask* mask,
+                           float scale, int32_t max_q, attn_tensor* o, attn_tensor* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  attn::ForgetKernelEvents forget_events;
+  attn_status st = check_mask(mask);
+  if (st != ATTN_OK) return st;
+  if (flags_of(mask) & ~(ATTN_MASK_CAUSAL | ATTN_MASK_WINDOW | ATTN_MASK_FIRST)) return ATTN_ERR_UNSUPPORTED;
+  if (mask && mask->dropout_p != 0.f) return ATTN_ERR_UNSUPPORTED;
+  PagedP p;
+  if ((st = check_cache(cache, p.c)) != ATTN_OK) return st;
+  if (!q || !o || !lse || q->ndim != 3 || !dims_fit_int(q) || !isfinite(scale) || max_q < 0) return ATTN_ERR_INVALID_ARG;
+  if (!matches_cache(q->dtype, p.c) || o->dtype != q->dtype || lse->dtype != ATTN_F32) return ATTN_ERR_INVALID_ARG;
+  const int64_t rows = q->shape[0], Hq = q->shape[1];
+  const int64_t qs[3] = {rows, Hq, p.c.d}, os[3] = {rows, Hq, p.c.dv}, ls[2] = {rows, Hq};
+  if (!same_shape(q, 3, qs) || !inner_contiguous(q) || Hq < 1 || Hq % p.c.Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (rows && !q->data) return ATTN_ERR_INVALID_ARG;
+  if ((st = check_pool(o, 3, os, true)) != ATTN_OK || (st = check_pool(lse, 2, ls, false)) != ATTN_OK) return st;
+  if ((st = check_rows(rows, cu_q, p.c)) != ATTN_OK) return st;
+  if (rows * Hq >= kMaxRowWarps) return ATTN_ERR_UNSUPPORTED;
+  const size_t need = attn_paged_workspace_size(q, cache, mask);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != ATTN_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(workspace, 0, kStatusBytes, cs) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (!rows || !p.c.batch) return ATTN_OK;
+  p.c.status = static_cast<uint32_t*>(workspace);
+  p.q = q->data;
+  p.o = o->data;
+  p.lse = static_cast<float*>(lse->data);
+  for (int i = 0; i < 2; ++i) {
+    p.sq[i] = q->stride[i];
+    p.so[i] = o->stride[i];
+    p.sl[i] = lse->stride[i];
+  }
+  p.Hq = (int32_t)Hq;
+  p.dtype = q->dtype;
+  const MaskP m = mask_params(mask);
+  p.flags = m.flags;
+  p.window = m.window < 0x7fffffff ? m.window : 0x7fffffff;
+  p.first = m.first;
+  p.sink = m.sink;
+  p.lse_fmt = m.lse_fmt;
+  p.scale = scale;
+  main_kernel_begin(cs);
+  const cudaError_t e = launch_paged_rows(p, cs);
+  main_kernel_end(cs);
   return cuda_status(e);
 }
 

@@ -33,6 +33,7 @@ struct MaskP {
   const int32_t* starts;   // (b, i) at starts[b * st_sb + i]: lowest allowed key, or null
   int64_t st_sb;
   uint32_t lse_fmt;        // ATTN_LSE_* bits of the LSE output
+  int64_t first;           // keys j < first are exempt from the window (0: none)
 };
 
 // Active length of batch row b, clamped to [0, n] (n when not set).
@@ -108,7 +109,7 @@ __device__ __forceinline__ void st(__half* p, float x) { *p = __float2half_rn(x)
 __device__ __forceinline__ bool allowed(const MaskP& m, int b, int h, int64_t i, int64_t j) {
   const int64_t ip = i + m.qoff;  // the query's key position
   if ((m.flags & ATTN_MASK_CAUSAL) && j > ip) return false;
-  if ((m.flags & ATTN_MASK_WINDOW) && j <= ip - m.window) return false;
+  if ((m.flags & ATTN_MASK_WINDOW) && j <= ip - m.window && j >= m.first) return false;
   if (m.flags & ATTN_MASK_BLOCK) {
     const uint8_t* row = m.bm + b * m.bm_sb + h * m.bm_sh + (i / m.bq) * m.bm_sq;
     if (!row[j / m.bk]) return false;
@@ -130,7 +131,7 @@ __device__ __forceinline__ void key_range(const MaskP& m, int b, int64_t i, int6
   if (m.flags & ATTN_MASK_CAUSAL) hi = ip < hi ? ip : hi;
   if (m.flags & ATTN_MASK_WINDOW) {
     int64_t w = ip - m.window + 1;
-    lo = w > 0 ? w : 0;
+    lo = w > 0 && !m.first ? w : 0;  // with first keys the range has a gap: skip_gap
   }
   if (m.lengths) {
     const int64_t L = active_len(m, b, n_k);
@@ -143,13 +144,20 @@ __device__ __forceinline__ void key_range(const MaskP& m, int b, int64_t i, int6
   }
 }
 
+// The key to look at in place of key j of query row i: j itself, or, in the
+// gap between the first keys and the window, the window's lowest key.
+__device__ __forceinline__ int64_t skip_gap(const MaskP& m, int64_t i, int64_t j) {
+  const int64_t w = i + m.qoff - m.window + 1;
+  return m.first && j >= m.first && j < w ? w : j;
+}
+
 // Query range [lo, hi] that can hold key j in its allowed set.
 __device__ __forceinline__ void query_range(const MaskP& m, int b, int64_t j, int64_t n_q,
                                             int64_t& lo, int64_t& hi) {
   lo = 0;
   hi = n_q - 1;
   if (m.flags & ATTN_MASK_CAUSAL) lo = j - m.qoff > 0 ? j - m.qoff : 0;
-  if (m.flags & ATTN_MASK_WINDOW) {
+  if ((m.flags & ATTN_MASK_WINDOW) && j >= m.first) {
     int64_t w = j + m.window - 1 - m.qoff;
     hi = w < hi ? w : hi;
   }

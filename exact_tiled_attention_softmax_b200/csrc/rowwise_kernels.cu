@@ -79,6 +79,7 @@ dense_fwd_rows(DenseP p, T* o, int64_t so0, int64_t so1, int64_t so2, float* lse
   int64_t lo, hi;
   key_range(p.m, b, i, p.Tk, lo, hi);
   for (int64_t j = lo; j <= hi; ++j) {
+    if ((j = skip_gap(p.m, i, j)) > hi) break;
     if (!allowed(p.m, b, h, i, j)) continue;  // empty keys leave the state untouched
     float kr[NQ];
     load_row(Kb + j * p.sk[2], p.d, lane, kr);
@@ -195,6 +196,7 @@ dense_dq_rows(DenseP p, const T* g, int64_t sg0, int64_t sg1, int64_t sg2, const
     int64_t lo, hi;
     key_range(p.m, b, i, p.Tk, lo, hi);
     for (int64_t j = lo; j <= hi; ++j) {
+      if ((j = skip_gap(p.m, i, j)) > hi) break;
       if (!allowed(p.m, b, h, i, j)) continue;
       float kr[NQ], vr[NV];
       load_row(Kb + j * p.sk[2], p.d, lane, kr);

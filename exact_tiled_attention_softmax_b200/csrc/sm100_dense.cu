@@ -60,17 +60,19 @@ enum : uint8_t { kEmpty = 0, kFull = 1, kPartial = 2 };
 // Is every (i, j) of the rectangle [r0, r1] x [c0, c1] inside the
 // causal/window band, and is any? Rows are given as key positions (query row
 // + qoff). Row i allows [max(c0, i-W+1), min(c1, i)], so some row qualifies
-// iff i can be chosen with c0 <= i (causal) and i <= c1 + W - 1 (window).
+// iff i can be chosen with c0 <= i (causal) and i <= c1 + W - 1 (window). The
+// window does not apply to columns below m.first (0 when not set).
 __device__ __forceinline__ void band_test(const MaskP& m, int64_t r0, int64_t r1, int64_t c0, int64_t c1, bool& any,
                                           bool& all) {
   const bool causal = m.flags & ATTN_MASK_CAUSAL, window = m.flags & ATTN_MASK_WINDOW;
   all = true;
   if (causal && c1 > r0) all = false;
-  if (window && c0 < r1 - m.window + 1) all = false;
+  if (window && c1 >= m.first && (c0 > m.first ? c0 : m.first) < r1 - m.window + 1) all = false;
   int64_t lo = r0, hi = r1;
   if (causal && c0 > lo) lo = c0;
   if (window && c1 + m.window - 1 < hi) hi = c1 + m.window - 1;
   any = c0 <= c1 && lo <= hi;
+  if (c0 < m.first && c0 <= c1 && r0 <= r1 && (!causal || c0 <= r1)) any = true;
 }
 
 // Class of the (64-row query slice qs, 128-key tile kt) pair.
@@ -231,7 +233,7 @@ __device__ __forceinline__ void fwd_key_tiles(const MaskP& m, int b, int Tq, int
   }
   if (m.flags & ATTN_MASK_WINDOW) {
     const int64_t first = (int64_t)q0 + m.qoff - m.window + 1;
-    lo = first > 0 ? (int)(first / kBN) : 0;
+    lo = first > 0 && !m.first ? (int)(first / kBN) : 0;  // with first keys: FwdGap
   }
   if (m.lengths) {  // Tq = Tk here
     const int64_t L = active_len(m, b, Tk);
@@ -240,6 +242,22 @@ __device__ __forceinline__ void fwd_key_tiles(const MaskP& m, int b, int Tq, int
     else if ((L - 1) / kBN < hi)
       hi = (int)((L - 1) / kBN);
   }
+}
+
+// Key tiles [lo, hi) between the first keys and the window of the query rows
+// from q0 on: empty for every row, and stepped over as a whole, so that a row
+// block's walk costs its own tiles and not the sequence's length. lo = -1
+// when there is no gap.
+struct FwdGap {
+  int lo, hi;
+};
+
+__device__ __forceinline__ FwdGap fwd_gap(const MaskP& m, int q0) {
+  FwdGap g{-1, -1};
+  const int64_t w = (int64_t)q0 + m.qoff - m.window + 1;  // the lowest key of the first row's window
+  const int64_t f = (m.first + kBN - 1) / kBN;
+  if (m.first && w / kBN > f) g = FwdGap{(int)f, (int)(w / kBN)};
+  return g;
 }
 
 // Class of (128-row query tile qt, key tile kt); tiles past Tq are empty.
@@ -251,9 +269,10 @@ __device__ __forceinline__ uint8_t wg_class(const FwdArgs& a, int b, int h, int 
 // First key tile after `from` (up to kt_hi) with allowed keys for either
 // query tile of the CTA (qt0, qt0 + 1); kt_hi + 1 when none. flags: bit w
 // set when query tile qt0 + w has allowed keys there.
-__device__ __forceinline__ int fwd_next_tile(const FwdArgs& a, int b, int h, int qt0, int kt_hi, int from,
-                                             uint32_t& flags) {
+__device__ __forceinline__ int fwd_next_tile(const FwdArgs& a, int b, int h, int qt0, const FwdGap& gap, int kt_hi,
+                                             int from, uint32_t& flags) {
   for (int kt = from + 1; kt <= kt_hi; ++kt) {
+    if (kt == gap.lo && (kt = gap.hi) > kt_hi) break;
     flags = (wg_class(a, b, h, qt0, kt) != kEmpty ? 1u : 0u) | (wg_class(a, b, h, qt0 + 1, kt) != kEmpty ? 2u : 0u);
     if (flags) return kt;
   }
@@ -311,9 +330,14 @@ __device__ __forceinline__ void fwd_row_bits(const FwdArgs& a, int b, int h, int
     lo = iv.lo;
     hi = iv.hi;
   }
-  if (lo > hi) return;
+  if (lo > hi && !a.m.first) return;
   w0 = range_bits64(lo - j0, hi - j0);
   w1 = range_bits64(lo - j0 - 64, hi - j0 - 64);
+  if (j0 < a.m.first) {  // the tile's first keys, which the window does not bound
+    const int64_t fh = a.m.first - 1 < hi ? a.m.first - 1 : hi;
+    w0 |= range_bits64(0, fh - j0);
+    w1 |= range_bits64(-64, fh - j0 - 64);
+  }
   if ((a.m.flags & ATTN_MASK_BLOCK) && !a.block_aligned) {
     const uint8_t* row = a.m.bm + b * a.m.bm_sb + h * a.m.bm_sh + (i / a.m.bq) * a.m.bm_sq;
     uint64_t b0 = 0, b1 = 0;
@@ -592,6 +616,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
   const int qt0 = 2 * ct;
   int kt_lo, kt_hi;
   fwd_key_tiles(a.m, b, a.Tq, a.Tk, q0, kFwdRows, kt_lo, kt_hi);
+  const FwdGap gap = fwd_gap(a.m, q0);
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ctl->q_full), 1);
@@ -634,9 +659,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
     // issuer, which reads each stage's flags from tinfo.
     int n = 0;
     uint32_t fl;
-    for (int kt = fwd_next_tile(a, b, h, qt0, kt_hi, kt_lo - 1, fl); kt <= kt_hi;) {
+    for (int kt = fwd_next_tile(a, b, h, qt0, gap, kt_hi, kt_lo - 1, fl); kt <= kt_hi;) {
       uint32_t nfl;
-      const int nk = fwd_next_tile(a, b, h, qt0, kt_hi, kt, nfl);
+      const int nk = fwd_next_tile(a, b, h, qt0, gap, kt_hi, kt, nfl);
       const int s = n % kStages;
       if (!wait_bar(smem_u32(&ctl->kv_empty[s]), ((n / kStages) & 1) ^ 1, abort_flag, a.status)) break;
       ctl->tinfo[s] = fl | (nk <= kt_hi ? 4u : 0u);  // published by the release of the arrive below
@@ -684,7 +709,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
       __syncwarp();
     };
     uint32_t fl0;
-    const bool any = fwd_next_tile(a, b, h, qt0, kt_hi, kt_lo - 1, fl0) <= kt_hi;
+    const bool any = fwd_next_tile(a, b, h, qt0, gap, kt_hi, kt_lo - 1, fl0) <= kt_hi;
     uint32_t info = 0;
     int npv[2] = {0, 0};
     int n = 0;
@@ -755,6 +780,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
     int cbase = kt_lo - 32;
     uint32_t cword = 0;
     for (int kt = kt_lo; kt <= kt_hi && ok; ++kt) {
+      if (kt == gap.lo && (kt = gap.hi) > kt_hi) break;
       if (kt - cbase >= 32) {
         cbase = kt;
         const int mk = kt + lane;
@@ -921,7 +947,7 @@ __device__ __forceinline__ void bwd_query_slices(const MaskP& m, int b, int Tq, 
     const int64_t first = (int64_t)k0 - m.qoff;
     if (first > 0) lo = first / kBMb < nqs ? (int)(first / kBMb) : nqs;
   }
-  if (m.flags & ATTN_MASK_WINDOW) {  // rows whose window still reaches the tile's last key
+  if ((m.flags & ATTN_MASK_WINDOW) && k0 >= m.first) {  // rows whose window still reaches the tile's last key
     const int64_t last = (int64_t)k0 + kBN - 1 + m.window - 1 - m.qoff;
     if (last < 0)
       hi = -1;
@@ -979,7 +1005,7 @@ __device__ __forceinline__ uint64_t bwd_col_bits(const BwdArgs& a, int b, int h,
   int64_t lo = i0, hi = i0 + kBMb - 1;
   if (hi > a.Tq - 1) hi = a.Tq - 1;
   if (a.m.flags & ATTN_MASK_CAUSAL) lo = j - a.m.qoff > lo ? j - a.m.qoff : lo;  // row i sees j iff i + qoff >= j
-  if (a.m.flags & ATTN_MASK_WINDOW)
+  if ((a.m.flags & ATTN_MASK_WINDOW) && j >= a.m.first)
     hi = j + a.m.window - 1 - a.m.qoff < hi ? j + a.m.window - 1 - a.m.qoff : hi;
   uint64_t w = range_bits64(lo - i0, hi - i0);
   if (w && (a.m.flags & (ATTN_MASK_LENGTHS | ATTN_MASK_STARTS))) w &= col_rows_allowed(a.m.lengths, a.m.starts, a.m.st_sb, b, i0, j, a.Tq);
@@ -1517,9 +1543,12 @@ struct DqCtl {
 
 // Next key tile after `from` (up to kt_hi) with allowed keys for query tile
 // qt; kt_hi + 1 when none. Every role walks the same sequence.
-__device__ __forceinline__ int dq_next_tile(const FwdArgs& a, int b, int h, int qt, int kt_hi, int from) {
-  for (int kt = from + 1; kt <= kt_hi; ++kt)
+__device__ __forceinline__ int dq_next_tile(const FwdArgs& a, int b, int h, int qt, const FwdGap& gap, int kt_hi,
+                                            int from) {
+  for (int kt = from + 1; kt <= kt_hi; ++kt) {
+    if (kt == gap.lo && (kt = gap.hi) > kt_hi) break;
     if (wg_class(a, b, h, qt, kt) != kEmpty) return kt;
+  }
   return kt_hi + 1;
 }
 
@@ -1543,6 +1572,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
   const int q0 = qt * kBM;
   int kt_lo, kt_hi;
   fwd_key_tiles(f.m, b, f.Tq, f.Tk, q0, kBM, kt_lo, kt_hi);
+  const FwdGap gap = fwd_gap(f.m, q0);
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ctl->q_full), 1);
@@ -1567,7 +1597,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int first = dq_next_tile(f, b, h, qt, kt_hi, kt_lo - 1);
+  const int first = dq_next_tile(f, b, h, qt, gap, kt_hi, kt_lo - 1);
 
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer
@@ -1582,7 +1612,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     tma_load_4d(sbase + kDqG, &tg, qf, 0, q0, h, b);
     tma_load_4d(sbase + kDqG + kTileBytes / 2, &tg, qf, 64, q0, h, b);
     int n = 0;
-    for (int kt = first; kt <= kt_hi; kt = dq_next_tile(f, b, h, qt, kt_hi, kt), ++n) {
+    for (int kt = first; kt <= kt_hi; kt = dq_next_tile(f, b, h, qt, gap, kt_hi, kt), ++n) {
       const int s = n % kStages;
       if (!wait_bar(smem_u32(&ctl->kv_empty[s]), ((n / kStages) & 1) ^ 1, abort_flag, f.status)) break;
       const uint32_t kf = smem_u32(&ctl->k_full[s]), vf = smem_u32(&ctl->v_full[s]);
@@ -1645,7 +1675,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
       }
     }
     for (int kt = first; ok && kt <= kt_hi; ++n) {
-      const int nk = dq_next_tile(f, b, h, qt, kt_hi, kt);
+      const int nk = dq_next_tile(f, b, h, qt, gap, kt_hi, kt);
       const int s = n % kStages, s1 = (n + 1) % kStages;
       const bool more = nk <= kt_hi;
       if (more) {  // S of the next tile into the other buffer while the warps work on this one
@@ -1693,6 +1723,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     int cbase = kt_lo - 32;
     uint32_t cword = 0;
     for (int kt = kt_lo; ok && kt <= kt_hi; ++kt) {
+      if (kt == gap.lo && (kt = gap.hi) > kt_hi) break;
       if (kt - cbase >= 32) {
         cbase = kt;
         const int mk = kt + lane;

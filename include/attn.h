@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define ATTN_VERSION 107 /* major * 100 + minor */
+#define ATTN_VERSION 108 /* major * 100 + minor */
 
 typedef enum attn_status {
   ATTN_OK = 0,
@@ -70,6 +70,8 @@ typedef enum attn_status {
 #define ATTN_DEVERR_TIMEOUT 0x4u     /* a bounded pipeline wait gave up */
 #define ATTN_DEVERR_TOPK_CAUSAL 0x8u /* ATTN_MASK_TOPK_CHECK_CAUSAL: a listed index lies
                                         beyond its token's causal position */
+#define ATTN_DEVERR_PAGE 0x10u   /* a page number outside the pool; its positions were left out */
+#define ATTN_DEVERR_RAGGED 0x20u /* cu_q or seq_lens out of range (clamped, see attn_cache) */
 /* ATTN_DEVERR_OVERFLOW: when the top-k reverse pass sums each dKV element in
  * a signed 32.32 fixed-point integer (range +-2^31: the row kernels, and the
  * tensor-core path under ATTN_BWD_DETERMINISTIC), the bit is set when a
@@ -79,7 +81,9 @@ typedef enum attn_status {
  * every overflow exceeds, so a sum that wrapped always sets the bit (the
  * bound can also set it for sums that did fit). */
 
-typedef enum attn_dtype { ATTN_F32 = 0, ATTN_BF16 = 1, ATTN_F16 = 2 } attn_dtype;
+/* ATTN_E4M3 (8-bit floating point: 4 exponent bits, 3 fraction bits, largest
+ * finite value 448) is a storage type of paged caches only. */
+typedef enum attn_dtype { ATTN_F32 = 0, ATTN_BF16 = 1, ATTN_F16 = 2, ATTN_E4M3 = 3 } attn_dtype;
 
 /* A strided tensor view. Strides count elements, not bytes; the innermost
  * dimension must have stride 1. Unused trailing entries are ignored. */
@@ -108,6 +112,11 @@ typedef struct attn_tensor {
  * caller's contract, and the check reports a broken one without changing the
  * result. Costs one compare per listed entry. */
 #define ATTN_MASK_TOPK_CHECK_CAUSAL 0x40u
+/* First tokens that stay visible: the window does not apply to keys
+ * j < window_first, so with ATTN_MASK_WINDOW (required) the window's set is
+ * { j > p(i) - window_left } united with { j < window_first }; every other
+ * set still intersects. Not with ATTN_MASK_STARTS (ATTN_ERR_UNSUPPORTED). */
+#define ATTN_MASK_FIRST 0x80u
 
 /* The allowed-set descriptor ("Tiled attention and its recomputed reverse
  * pass are exact": the fixed allowed sets A_i; causal, windowed and packed
@@ -161,6 +170,9 @@ typedef struct attn_mask {
   uint32_t lse_format;
   /* Options of attn_bwd: 0 or ATTN_BWD_DETERMINISTIC. */
   uint32_t bwd_flags;
+  /* ATTN_MASK_FIRST: the number of first keys the window leaves visible,
+   * >= 0 (read only when the flag is set). */
+  int64_t window_first;
 } attn_mask;
 
 /* ATTN_BWD_DETERMINISTIC: every gradient is bitwise reproducible from run to
@@ -261,6 +273,84 @@ attn_status attn_bwd_noalloc(const attn_tensor* q, const attn_tensor* k,
                              const attn_mask* mask, float scale, attn_tensor* dq,
                              attn_tensor* dk, attn_tensor* dv, float* dsink,
                              void* stream);
+
+/* ------------------------------------------------------------ paged caches
+ *
+ * A paged K/V cache: a pool of pages of page_size cached positions each, and
+ * per sequence the list of the pages that hold its positions 0 .. seq_len - 1
+ * (position p sits in page block_table[b][p / page_size] at p % page_size).
+ * The same descriptor serves the three calls below. A step of serving writes
+ * the step's new tokens with attn_cache_write and then attends with
+ * attn_paged_fwd, both with the same cu_q and with seq_lens that already count
+ * the new tokens: sequence b's n_b = cu_q[b+1] - cu_q[b] new tokens (0 is
+ * allowed) sit at positions seq_lens[b] - n_b .. seq_lens[b] - 1. cu_q is
+ * int32 [batch + 1]; NULL means that every sequence brings the same number
+ * (rows / batch) of tokens.
+ *
+ * Pool: k [num_pages, page_size, Hkv, d], v [num_pages, page_size, Hkv, dv],
+ * any stride order with the innermost dimension contiguous (a pool laid out
+ * [num_pages][Hkv][page_size][d] is a transposed view). dtype: ATTN_F32,
+ * ATTN_BF16, ATTN_F16, or ATTN_E4M3 with k_scale, v_scale fp32
+ * [num_pages, page_size, Hkv], any strides: the cached row stands for
+ * code * scale. For the other types the scales' data pointers are NULL.
+ *
+ * Values only the device sees are checked there and reported in the status
+ * word when the call has a workspace: positions in a page number outside
+ * [0, num_pages) (or past max_pages pages) belong to no set, are not written
+ * and not read back (ATTN_DEVERR_PAGE); seq_lens and cu_q are clamped to
+ * [0, max_pages * page_size] and [0, rows], and new tokens at negative
+ * positions (n_b > seq_lens[b]) are not written and see no key
+ * (ATTN_DEVERR_RAGGED for all of these). Rows of q, k, v, o and lse that
+ * belong to no sequence (past cu_q[batch]) are neither read nor written. */
+typedef struct attn_cache {
+  attn_tensor k, v;
+  attn_tensor k_scale, v_scale;
+  const int32_t* block_table; /* [batch, max_pages], row stride table_stride */
+  int64_t table_stride;
+  int32_t max_pages;
+  int32_t batch;
+  const int32_t* seq_lens; /* [batch] */
+} attn_cache;
+
+/* Writes the new tokens' rows k [rows, Hkv, d], v [rows, Hkv, dv] into the
+ * cache. The rows' dtype is the cache's, or, for an ATTN_E4M3 cache, any of
+ * the other three: each row x is then stored as scale = max|x| / 448 (1 for a
+ * row of zeros) and e4m3(x / scale), rounded to nearest even; a row that
+ * holds an infinity or a NaN gets a non-finite scale and reads back as NaN
+ * throughout. A page position must be written by one token only: pages
+ * shared between sequences hold whichever token was stored last.
+ * workspace: NULL (device checks are then applied but not reported), or at
+ * least 256 bytes for the status word. */
+attn_status attn_cache_write(const attn_tensor* k, const attn_tensor* v, const int32_t* cu_q,
+                             const attn_cache* cache, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Reads the cache back into the dense layout of attn_fwd and attn_bwd:
+ * k [batch, Hkv, T, d], v [batch, Hkv, T, dv] of dtype ATTN_F32, ATTN_BF16 or
+ * ATTN_F16 (an unquantised cache's own dtype only). Rows
+ * j < min(seq_lens[b], T) are written; the others are left as they were.
+ * workspace as in attn_cache_write. */
+attn_status attn_cache_read(const attn_cache* cache, attn_tensor* k, attn_tensor* v, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_paged_fwd needs (>= 256) on the current device. */
+size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, const attn_mask* mask);
+
+/* Attention of the new tokens over the cache: q, o [rows, Hq, d / dv], lse
+ * fp32 [rows, Hq]. Query i of sequence b's new tokens sits at key position
+ * p(i) = seq_lens[b] - n_b + i; its allowed set is the keys j < seq_lens[b]
+ * intersected with the mask's sets: ATTN_MASK_CAUSAL, ATTN_MASK_WINDOW,
+ * ATTN_MASK_FIRST, and sink and lse_format; other flags and dropout are
+ * ATTN_ERR_UNSUPPORTED. q's dtype is the cache's, or for an ATTN_E4M3 cache any
+ * of the other three; o's is q's. Scores take the cached code times its
+ * scale exactly (the scale multiplies the fp32 score, and the probability in
+ * front of the value row). Infinities and NaN in rows a query does not see
+ * do not reach it. A row whose allowed scores are all -inf counts as empty.
+ * max_q: the largest n_b, if the caller knows it, else 0: it chooses
+ * between kernels and never changes which tokens are attended. The result is
+ * bitwise reproducible for the same arguments on the same device. */
+attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn_cache* cache,
+                           const attn_mask* mask, float scale, int32_t max_q, attn_tensor* o, attn_tensor* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, then reads and clears the device status word at the
  * start of `workspace` (workspace NULL: the status word of attn_bwd_noalloc's

@@ -1,0 +1,438 @@
+"""Paged caches on the GPU: the write, the read back and the attention over a
+cache against their float64 definitions, at the sizes and masks where they can
+go wrong, and a serving run of them together."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+import exact_tiled_attention_softmax_b200 as eta  # noqa: E402
+from tests.paged_util import (DT, E4M3, check, cu_of, make_cache, quantise, reference, run,  # noqa: E402
+                              seeded_q)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    eta.load_library()
+
+
+def bits(t):
+    return t.contiguous().view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]).cpu()
+
+
+# ------------------------------------------------------------- write, read
+
+
+WRITES = {
+    "one_token_each": dict(lens=[1, 17, 40, 64], new=[1, 1, 1, 1], page=16, Hkv=8, d=128, dv=128),
+    "ragged_with_none": dict(lens=[33, 20, 5, 130], new=[33, 0, 2, 70], page=32, Hkv=3, d=128, dv=128),
+    "wide_and_narrow_heads": dict(lens=[50, 9], new=[30, 9], page=64, Hkv=2, d=576, dv=72),
+    "odd_width": dict(lens=[50, 9], new=[30, 9], page=5, Hkv=2, d=33, dv=20),
+}
+
+
+@pytest.mark.parametrize("heads_first", [True, False])
+@pytest.mark.parametrize("src,store", [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32"), ("bf16", "e4m3"),
+                                       ("f16", "e4m3"), ("f32", "e4m3")])
+@pytest.mark.parametrize("kind", list(WRITES))
+def test_write_then_read(kind, src, store, heads_first):
+    c = WRITES[kind]
+    cache, _, _ = make_cache(c["lens"], c["page"], c["Hkv"], c["d"], c["dv"], DT[store], heads_first=heads_first, seed=3)
+    before = [bits(t) for t in cache.tensors()]
+    rows = sum(c["new"])
+    k, v = seeded_q(rows + 2, c["Hkv"], c["d"], DT[src], 5), seeded_q(rows + 2, c["Hkv"], c["dv"], DT[src], 6)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    eta.attn_cache_write(k, v, cache, cu_of(c["new"]), workspace=ws)
+    assert eta.attn_get_status(ws) == 0
+    # what the pool holds now: the new rows at their slots, all else as it was
+    want = [t.clone() for t in before]
+    table, at = cache.block_table.cpu(), 0
+    for b, (n, L) in enumerate(zip(c["new"], c["lens"])):
+        pos = torch.arange(L - n, L)
+        pg, off = table[b].long()[pos // c["page"]], pos % c["page"]
+        for i, new in enumerate((k, v)):
+            r = new[at:at + n].cpu()
+            if store == "e4m3":
+                code, s = quantise(r)
+                want[i][pg, off] = code.view(torch.uint8)
+                want[4 + i][pg, off] = s.view(torch.int32)
+            else:
+                want[i][pg, off] = bits(r)
+        at += n
+    for got, w in zip(cache.tensors(), want):
+        assert torch.equal(bits(got), w)
+    # and back: every row the sequences hold, the rows past them untouched
+    T = max(c["lens"]) + 3
+    for out in (["bf16", "f16", "f32"] if store == "e4m3" else [store]):
+        B = len(c["lens"])
+        ok = torch.full((B, T, c["Hkv"], c["d"]), 7.0, dtype=DT[out], device="cuda").transpose(1, 2)
+        ov = torch.full((B, c["Hkv"], T, c["dv"]), 7.0, dtype=DT[out], device="cuda")
+        eta.attn_cache_read(cache, k=ok, v=ov, workspace=ws)
+        assert eta.attn_get_status(ws) == 0
+        for got, pool, scale in ((ok, cache.k, cache.k_scale), (ov, cache.v, cache.v_scale)):
+            vals = pool.float().cpu() if scale is None else pool.float().cpu() * scale.cpu()[..., None]
+            for b, L in enumerate(c["lens"]):
+                pos = torch.arange(L)
+                r = vals[table[b].long()[pos // c["page"]], pos % c["page"]].to(DT[out])
+                assert torch.equal(got[b, :, :L].cpu(), r.transpose(0, 1))
+                assert (got[b, :, L:] == 7).all()
+
+
+def test_write_of_special_rows():
+    """Zero rows, rows of the smallest values, and rows with an infinity or a
+    NaN: zeros stay zeros, finite rows stay finite, the others read as NaN."""
+    cache, _, _ = make_cache([6], 16, 1, 128, 128, E4M3, seed=1)
+    k = torch.zeros(6, 1, 128, device="cuda")
+    k[1, 0, 3] = 1e-45
+    k[1, 0, 4] = -0.0
+    k[2, 0, 5] = math.inf
+    k[3, 0, 6] = math.nan
+    k[4] = 3e38
+    k[5] = torch.linspace(-448, 448, 128)
+    eta.attn_cache_write(k, k, cache)
+    for got in eta.attn_cache_read(cache, 6, dtype=torch.float32):
+        got = got[0, 0].cpu()
+        assert (got[0] == 0).all() and (got[1] == 0).all()
+        assert torch.isnan(got[2]).all() and torch.isnan(got[3]).all()
+        # (3e38 / s) is 448 up to one rounding each way, and back times s
+        assert torch.allclose(got[4], torch.full((128,), 3e38), rtol=2.0 ** -22)
+        # e4m3: half a step relative, 2^-10 of the scale for the subnormal codes
+        assert ((got[5] - k[5, 0].cpu()).abs() <= k[5, 0].cpu().abs() * 2.0 ** -4 + 2.0 ** -10).all()
+
+
+def test_write_and_read_report_bad_pages_and_lengths():
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    cache, K, _ = make_cache([40, 20], 16, 2, 128, 128, torch.bfloat16, seed=2)
+    cache.block_table[0, 1] = cache.k.shape[0]  # one past the pool: positions 16..31 of sequence 0
+    before = bits(cache.k)
+    k = seeded_q(60, 2, 128, torch.bfloat16)
+    eta.attn_cache_write(k, k, cache, cu_of([40, 20]), workspace=ws)
+    assert eta.attn_get_status(ws) == eta.ATTN_DEVERR_PAGE
+    live = torch.zeros(cache.k.shape[0], 16, dtype=torch.bool)
+    for b, p in ((0, list(range(16)) + list(range(32, 40))), (1, list(range(20)))):
+        for x in p:
+            live[int(cache.block_table[b, x // 16]), x % 16] = True
+    assert torch.equal(bits(cache.k)[~live], before[~live])
+    out = [torch.full((2, 2, 48, 128), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    eta.attn_cache_read(cache, k=out[0], v=out[1], workspace=ws)
+    assert eta.attn_get_status(ws) == eta.ATTN_DEVERR_PAGE
+    assert (out[0][0, :, 16:32] == 9).all() and (out[0][0, :, 40:] == 9).all()
+    assert torch.equal(out[0][0, :, 32:40].transpose(0, 1), k[32:40])
+    # more new tokens than positions: the ones in front of position 0 go nowhere
+    cache, _, _ = make_cache([3, 20], 16, 2, 128, 128, torch.bfloat16, seed=2)
+    eta.attn_cache_write(k[:9], k[:9], cache, cu_of([5, 4]), workspace=ws)
+    assert eta.attn_get_status(ws) == eta.ATTN_DEVERR_RAGGED
+    got, _ = eta.attn_cache_read(cache, 3)
+    assert torch.equal(got[0].transpose(0, 1), k[2:5])
+    # lengths and offsets out of range are clamped
+    for lens, cu in (([-4, 20], [0, 0, 2]), ([1000, 20], [0, 0, 2]), ([3, 20], [0, -1, 2]), ([3, 20], [0, 2, 1000]),
+                     ([3, 20], [2, 1, 4])):
+        cache.seq_lens.copy_(torch.tensor(lens))
+        eta.attn_cache_write(k[:4], k[:4], cache, torch.tensor(cu, dtype=torch.int32, device="cuda"), workspace=ws)
+        assert eta.attn_get_status(ws) & eta.ATTN_DEVERR_RAGGED
+
+
+# --------------------------------------------------------------- attention
+
+
+ATTN = {
+    # every length from one key on, pages that end inside a tile, one token each
+    "decode": dict(lens=[1, 2, 15, 16, 17, 127, 128, 129, 300], new=[1] * 9, page=16, Hq=8, Hkv=2),
+    "decode_mha": dict(lens=[5, 260], new=[1, 1], page=32, Hq=4, Hkv=4),
+    "decode_mqa": dict(lens=[100, 33], new=[1, 1], page=64, Hq=16, Hkv=1),
+    "decode_wide_group": dict(lens=[100, 33], new=[1, 1], page=64, Hq=40, Hkv=1),
+    "few_tokens": dict(lens=[70, 4, 260, 9], new=[3, 4, 2, 0], page=16, Hq=12, Hkv=4),
+    "odd_group": dict(lens=[150, 40], new=[30, 40], page=16, Hq=9, Hkv=3),
+    "chunk": dict(lens=[300, 129, 64], new=[130, 129, 1], page=64, Hq=8, Hkv=2),
+    "chunk_page_128": dict(lens=[400], new=[257], page=128, Hq=4, Hkv=4),
+    "page_48": dict(lens=[400, 20], new=[5, 20], page=48, Hq=4, Hkv=2),
+    "page_256": dict(lens=[600, 20], new=[70, 2], page=256, Hq=4, Hkv=2),
+    "page_7": dict(lens=[60, 20], new=[5, 20], page=7, Hq=4, Hkv=2),
+    "page_1": dict(lens=[9, 3], new=[2, 1], page=1, Hq=4, Hkv=2),
+    "widths": dict(lens=[60, 20], new=[5, 20], page=16, Hq=4, Hkv=2, d=80, dv=48),
+    "wide": dict(lens=[40], new=[3], page=16, Hq=2, Hkv=1, d=576, dv=512),
+}
+MASKS = {
+    "causal": dict(causal=True),
+    "all_keys": dict(causal=False),
+    "window": dict(causal=True, window=20),
+    "window_first": dict(causal=True, window=33, first=5),
+    "window_first_many": dict(causal=True, window=1, first=150),
+    "open_window_first": dict(causal=False, window=7, first=3),
+}
+
+
+def allowed_of(mask, sink=None, **kw):
+    return eta.AllowedSet(causal=mask["causal"], window_left=mask.get("window", 0), window_first=mask.get("first", 0),
+                          sink=sink, **kw)
+
+
+def one_case(kind, qd, cd, mask, *, heads_first=True, sink=False, max_q=True, seed=0):
+    c = dict(dict(d=128, dv=128), **ATTN[kind])
+    cache, K, V = make_cache(c["lens"], c["page"], c["Hkv"], c["d"], c["dv"], DT[cd], heads_first=heads_first,
+                             seed=seed, src=DT[qd])
+    q = seeded_q(sum(c["new"]), c["Hq"], c["d"], DT[qd], seed + 1)
+    z = torch.randn(c["Hq"], generator=torch.Generator().manual_seed(seed)).cuda() if sink else None
+    o, lse = run(q, cache, c["new"], allowed=allowed_of(mask, z), max_q=max(c["new"]) if max_q else 0)
+    ref = reference(q, K, V, c["new"], c["lens"], c["d"] ** -0.5, sink=None if z is None else z.cpu(), **mask)
+    check(o, lse, *ref, tensor_core=qd != "f32")
+    return o, lse
+
+
+@pytest.mark.parametrize("kind", list(ATTN))
+@pytest.mark.parametrize("qd,cd", [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32"), ("bf16", "e4m3"), ("f16", "e4m3"),
+                                   ("f32", "e4m3")])
+def test_attention_types(kind, qd, cd):
+    one_case(kind, qd, cd, MASKS["causal"])
+
+
+@pytest.mark.parametrize("mask", list(MASKS))
+@pytest.mark.parametrize("kind", ["decode", "few_tokens", "odd_group", "chunk", "page_7"])
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+def test_attention_masks(kind, mask, cd):
+    one_case(kind, "bf16", cd, MASKS[mask], heads_first=False, sink=mask != "causal", seed=4)
+
+
+@pytest.mark.parametrize("kind", ["decode", "few_tokens", "chunk"])
+def test_max_q_changes_no_set(kind):
+    """Without the hint, and with a wrong one, the same tokens are attended."""
+    one_case(kind, "bf16", "bf16", MASKS["causal"], max_q=False)
+    c = ATTN[kind]
+    cache, K, V = make_cache(c["lens"], c["page"], c["Hkv"], 128, 128, torch.bfloat16)
+    q = seeded_q(sum(c["new"]), c["Hq"], 128, torch.bfloat16)
+    o, lse = run(q, cache, c["new"], allowed=eta.AllowedSet(causal=True), max_q=1)
+    check(o, lse, *reference(q, K, V, c["new"], c["lens"], 128 ** -0.5), tensor_core=True)
+
+
+@pytest.mark.parametrize("kind,new", [("decode", 1), ("few_tokens", 3), ("chunk", 60)])
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+def test_rows_outside_every_sequence_and_strides(kind, new, cd):
+    """Rows in front of the first sequence and behind the last stay as they
+    were; q, o and lse are strided views; cu_q does not start at 0."""
+    lens = [max(L, new) for L in ATTN[kind]["lens"]]
+    B, Hkv, Hq = len(lens), 2, 8
+    cache, K, V = make_cache(lens, 16, Hkv, 128, 128, DT[cd], seed=9)
+    rows = B * new + 5
+    q = seeded_q(rows, 2 * Hq, 128, torch.bfloat16)[:, ::2]
+    o = torch.full((Hq, rows, 136), 5.0, dtype=torch.bfloat16, device="cuda").transpose(0, 1)[..., :128]
+    lse = torch.full((Hq, rows), 5.0, device="cuda").t()
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * new + 2
+    ws = torch.empty(eta.attn_paged_workspace_size(q, cache), dtype=torch.uint8, device="cuda")
+    eta.attn_paged_fwd(q, cache, cu, eta.AllowedSet(causal=True), out=o, lse=lse, workspace=ws, max_q=new)
+    assert eta.attn_get_status(ws) == 0
+    ref = reference(q[2:-3], K, V, [new] * B, lens, 128 ** -0.5)
+    check(o[2:-3], lse[2:-3], *ref, tensor_core=True)
+    for part in (o[:2], o[-3:], lse[:2], lse[-3:]):
+        assert (part == 5).all()
+    # without cu_q: the same number each
+    o2, lse2 = run(q[2:-3], cache, allowed=eta.AllowedSet(causal=True), max_q=new)
+    check(o2, lse2, *ref, tensor_core=True)
+
+
+@pytest.mark.parametrize("fmt", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("kind", ["decode", "chunk", "page_7"])
+def test_lse_formats(kind, fmt):
+    c = ATTN[kind]
+    cache, K, V = make_cache(c["lens"], c["page"], c["Hkv"], 128, 128, torch.float16)
+    q = seeded_q(sum(c["new"]), c["Hq"], 128, torch.float16)
+    z = torch.randn(c["Hq"], device="cuda")
+    o, lse = run(q, cache, c["new"], allowed=eta.AllowedSet(causal=True, sink=z, lse_kv_only=fmt[0], lse_neg_log2=fmt[1]))
+    o_ref, l_ref, A = reference(q, K, V, c["new"], c["lens"], 128 ** -0.5, sink=z.cpu())
+    if fmt[0]:
+        l_ref = reference(q, K, V, c["new"], c["lens"], 128 ** -0.5)[1]
+    check(o, lse * -math.log(2) if fmt[1] else lse, o_ref, l_ref, A, tensor_core=True)
+
+
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind,new", [("decode", 1), ("few", 3), ("chunk", 140), ("any", 4)])
+def test_empty_rows_and_bad_pages(kind, new, cd):
+    """Sequences of length zero, tokens in front of position 0, pages outside
+    the pool: empty rows are 0 and -inf (or the sink), the rest is exact."""
+    page = 7 if kind == "any" else 16
+    lens = [300, 2, 300]
+    cache, K, V = make_cache(lens, page, 2, 128, 128, DT[cd], seed=5)
+    q = seeded_q(3 * new, 4, 128, torch.bfloat16)
+    bad = [1, 6]
+    for p, v in zip(bad, (-1, cache.k.shape[0] + 5)):
+        cache.block_table[2, p] = v
+    skip = [None, None, {x for p in bad for x in range(p * page, p * page + page)}]
+    cache.block_table[0] = -1
+    cache.seq_lens[0] = 0
+    want = eta.ATTN_DEVERR_PAGE | eta.ATTN_DEVERR_RAGGED
+    for sink in (None, torch.randn(4, device="cuda")):
+        o, lse = run(q, cache, [new] * 3, allowed=eta.AllowedSet(causal=True, sink=sink), max_q=new, status=want)
+        z = torch.full((4,), -math.inf) if sink is None else sink.cpu()
+        empty = new + max(0, new - 2)
+        assert (o[:empty] == 0).all()
+        assert torch.allclose(lse[:empty].cpu(), z.expand(empty, 4), rtol=2.0 ** -22, atol=0)
+        t = reference(q[empty:], K[1:], V[1:], [min(new, 2), new], [2, 300], 128 ** -0.5,
+                      sink=None if sink is None else sink.cpu(), skip=skip[1:])
+        check(o[empty:], lse[empty:], *t, tensor_core=True)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("kind,new", [("decode", 1), ("few", 4), ("chunk", 150), ("any", 4)])
+def test_masked_rows_hold_anything(kind, new, value):
+    """NaN and infinities in K and V rows that a query does not see do not
+    reach it; one that sees them is not finite."""
+    page = 7 if kind == "any" else 16
+    lens = [290, 290]
+    cache, K, V = make_cache(lens, page, 2, 128, 128, torch.bfloat16, seed=6)
+    hit = [100, 289, 270, 288]  # out of the window for all or some queries; after some queries
+    for j in hit:
+        pg, off = int(cache.block_table[0, j // page]), j % page
+        (cache.v if value != value or j % 2 == 0 else cache.k)[pg, off, 1, 3] = value
+        cache.v[pg, off, 1, 70] = value
+        V[0][j, 1, 70] = value
+    q = seeded_q(2 * new, 4, 128, torch.bfloat16)
+    mask = dict(causal=True, window=16, first=3)
+    o, lse = run(q, cache, [new, new], allowed=allowed_of(mask), max_q=new)
+    ok = torch.zeros(2 * new, 4, dtype=torch.bool)
+    for i in range(new):
+        p = 290 - new + i
+        ok[i] = not any(p - 16 < j <= p for j in hit)
+    ok[new:] = True
+    ok[:, :2] = True  # the first K/V head is clean
+    clean, Kc, Vc = make_cache(lens, page, 2, 128, 128, torch.bfloat16, seed=6)
+    ref = reference(q, Kc, Vc, [new, new], lens, 128 ** -0.5, **mask)
+    check(o[ok.cuda()], lse[ok.cuda()], *[r[ok] for r in ref], tensor_core=True)
+    assert not torch.isfinite(o[~ok.cuda()][:, 70]).any()
+
+
+def test_nan_scores_make_the_row_nan():
+    for new, page in ((1, 16), (150, 16), (2, 7)):
+        cache, _, _ = make_cache([300], page, 2, 128, 128, torch.bfloat16)
+        q = seeded_q(new, 4, 128, torch.bfloat16)
+        q[0] = math.nan
+        o, lse = run(q, cache, [new], allowed=eta.AllowedSet(causal=True), max_q=new)
+        assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+        assert torch.isfinite(o[1:]).all() and torch.isfinite(lse[1:]).all()
+
+
+@pytest.mark.parametrize("kind,new", [("decode", 1), ("chunk", 140)])
+def test_scores_of_large_spread(kind, new):
+    """Scores that grow along the keys move the running maximum in every tile;
+    scales of both signs."""
+    lens = [600, 350]
+    cache, K, V = make_cache(lens, 16, 2, 128, 128, torch.bfloat16, seed=8)
+    cache.k.zero_()
+    for b, L in enumerate(lens):
+        pos = torch.arange(L)
+        r = torch.zeros(L, 2, 128)
+        r[..., 0] = (pos.float() / 4).to(torch.bfloat16).float()[:, None]
+        K[b] = r.double()
+        cache.k[cache.block_table[b].long().cpu()[pos // 16].cuda(), (pos % 16).cuda()] = r.to(torch.bfloat16).cuda()
+    q = torch.zeros(2 * new, 4, 128, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    for scale in (1.0, -1.0):
+        o, lse = run(q, cache, [new, new], scale=scale, allowed=eta.AllowedSet(causal=True), max_q=new)
+        check(o, lse, *reference(q, K, V, [new, new], lens, scale), tensor_core=True)
+
+
+# ----------------------------------------------------- streams, graphs, runs
+
+
+def test_repeats_bitwise_and_on_other_streams():
+    for new in (1, 5, 200):
+        lens = [700, 301, 256]
+        cache, _, _ = make_cache(lens, 16, 2, 128, 128, torch.bfloat16)
+        q = seeded_q(3 * new, 8, 128, torch.bfloat16)
+        a = eta.AllowedSet(causal=True)
+        o, lse = run(q, cache, [new] * 3, allowed=a, max_q=new)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        got = []
+        for s in streams:  # three at once, workspaces of their own
+            got.append(eta.attn_paged_fwd(q, cache, cu_of([new] * 3), a, max_q=new, stream=s))
+        torch.cuda.synchronize()
+        for o2, lse2 in got:
+            assert torch.equal(bits(o), bits(o2)) and torch.equal(bits(lse), bits(lse2))
+
+
+@pytest.mark.parametrize("new", [1, 3, 140])
+def test_captured_step_replays_with_new_lengths(new):
+    """Write and attention captured once; two graphs share one workspace; the
+    lengths, tables and tokens change between replays."""
+    page, Hq, Hkv, B = 16, 8, 2, 2
+    cache, K, V = make_cache([400, 300], page, Hkv, 128, 128, E4M3, src=torch.bfloat16)
+    nk, nv = (torch.zeros(B * new, Hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros(B * new, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    a = eta.AllowedSet(causal=True, window_left=200, window_first=4)
+    ws = torch.empty(eta.attn_paged_workspace_size(q, cache, a), dtype=torch.uint8, device="cuda")
+    out = [(torch.empty_like(q), torch.empty(B * new, Hq, device="cuda")) for _ in range(2)]
+
+    def step(i):
+        eta.attn_cache_write(nk, nv, cache)
+        eta.attn_paged_fwd(q, cache, None, a, out=out[i][0], lse=out[i][1], workspace=ws, max_q=new)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step(0)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step(i)
+        graphs.append(g)
+    for t, (g, lens) in enumerate(zip(graphs * 2, ([400, 300], [150, 299], [new, 211], [399, 160]))):
+        cache.seq_lens.copy_(torch.tensor(lens))
+        for x, seed in ((nk, 50 + t), (nv, 60 + t), (q, 70 + t)):
+            x.copy_(seeded_q(*x.shape, torch.bfloat16, seed))
+        g.replay()
+        torch.cuda.synchronize()
+        for b in range(B):
+            for x, dense in ((nk, K), (nv, V)):
+                c, sc = quantise(x[b * new:(b + 1) * new].cpu())
+                dense[b][lens[b] - new:lens[b]] = c.double() * sc.double()[..., None]
+        ref = reference(q, [k[:L] for k, L in zip(K, lens)], [v[:L] for v, L in zip(V, lens)], [new] * B, lens,
+                        128 ** -0.5, window=200, first=4)
+        check(*out[t % 2], *ref, tensor_core=True)
+    assert eta.attn_get_status(ws) == 0
+
+
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+def test_serving_run(store):
+    """A prompt in chunks, then single tokens, each step written and attended,
+    against one dense forward pass over the rows read back at the end."""
+    B, Hq, Hkv, d, page = 2, 8, 2, 128, 16
+    total = [220, 90]
+    steps = [[100, 80], [90, 0], [27, 7]] + [[1, 1]] * 3
+    cache = eta.PagedCache.allocate(24, page, Hkv, d, B, 14, dtype=DT[store])
+    cache.block_table.copy_(torch.randperm(24, generator=torch.Generator().manual_seed(1))[:28 - 4].to(torch.int32)
+                            .repeat(2)[:28].reshape(2, 14).cuda())
+    cache.block_table[0] = torch.arange(0, 14)
+    cache.block_table[1] = torch.cat([torch.arange(14, 24), torch.arange(4) * 0 - 1])
+    g = torch.Generator().manual_seed(2)
+    qkv = [[torch.randn(L, h, d, generator=g).to(torch.bfloat16).cuda() for h in (Hq, Hkv, Hkv)] for L in total]
+    a = eta.AllowedSet(causal=True, window_left=64, window_first=4)
+    done, outs = [0, 0], [[], []]
+    for new in steps:
+        cat = [torch.cat([qkv[b][i][done[b]:done[b] + new[b]] for b in range(B)]) for i in range(3)]
+        cache.seq_lens.add_(torch.tensor(new, dtype=torch.int32, device="cuda"))
+        cu = cu_of(new)
+        eta.attn_cache_write(cat[1], cat[2], cache, cu)
+        o, _ = eta.attn_paged_fwd(cat[0], cache, cu, a, max_q=max(new))
+        at = 0
+        for b in range(B):
+            outs[b].append(o[at:at + new[b]])
+            at += new[b]
+            done[b] += new[b]
+    assert done == total
+    k, v = eta.attn_cache_read(cache, max(total), dtype=torch.float32 if store == "e4m3" else None)
+    for b in range(B):
+        L = total[b]
+        q = qkv[b][0].transpose(0, 1)[None]
+        kk, vv = k[b:b + 1, :, :L].float(), v[b:b + 1, :, :L].float()
+        want, lse = eta.attn_fwd(q.float(), kk.contiguous(), vv.contiguous(), a)
+        A, _ = eta.attn_fwd(q.float(), kk.contiguous(), vv.abs().contiguous(), a)
+        got = torch.cat(outs[b])
+        # the float32 dense pass stands 1e-5 from the definition (its own tests)
+        eps = 2.0 ** -8
+        want, A = want[0].transpose(0, 1), A[0].transpose(0, 1)
+        assert ((got.float() - want).abs() <= eps * want.abs() + (eps + 2.0 ** -12) * A + 2e-5).all()
