@@ -6,7 +6,7 @@
 
 #include "common.cuh"
 #include "launchers.h"
-#include "paged.cuh"
+#include "sm100_paged.h"
 #include "sm100_dense.h"
 #include "sm100_topk.h"
 
@@ -670,7 +670,8 @@ size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, 
   (void)q;
   (void)cache;
   (void)mask;
-  return kStatusBytes;
+  size_t zero;
+  return kStatusBytes + paged_decode_workspace_bytes(zero);
 }
 
 attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn_cache* cache, const attn_mask* mask,
@@ -695,8 +696,6 @@ attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn
   const size_t need = attn_paged_workspace_size(q, cache, mask);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != ATTN_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, kStatusBytes, cs) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (!rows || !p.c.batch) return ATTN_OK;
   p.c.status = static_cast<uint32_t*>(workspace);
   p.q = q->data;
   p.o = o->data;
@@ -715,8 +714,15 @@ attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn
   p.sink = m.sink;
   p.lse_fmt = m.lse_fmt;
   p.scale = scale;
+  const int64_t bound = max_q ? max_q : (cu_q || !p.c.batch ? rows : rows / p.c.batch);
+  const bool decode = paged_decode_supported(p, (int32_t)(bound < rows ? bound : rows));
+  size_t zero = 0;
+  if (decode) paged_decode_workspace_bytes(zero);
+  if (cudaMemsetAsync(workspace, 0, kStatusBytes + zero, cs) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (!rows || !p.c.batch) return ATTN_OK;
   main_kernel_begin(cs);
-  const cudaError_t e = launch_paged_rows(p, cs);
+  const cudaError_t e =
+      decode ? launch_paged_decode(p, static_cast<char*>(workspace) + kStatusBytes, cs) : launch_paged_rows(p, cs);
   main_kernel_end(cs);
   return cuda_status(e);
 }

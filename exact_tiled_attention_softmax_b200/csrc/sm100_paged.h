@@ -1,0 +1,20 @@
+// Tensor-core paths of attention over a paged cache (internal).
+#pragma once
+
+#include "paged.cuh"
+
+namespace attn {
+
+int sm_count();  // of the current device
+// Widths, types, page size and alignment that the tensor-core paths take.
+bool paged_pieces_ok(const PagedP& p);
+
+// Few new tokens a sequence: at most 16 rows (tokens x query heads of a
+// group) per K/V head. Bytes of workspace after the status block (counters
+// first, `zero` bytes of which must be cleared before the launch), and the
+// launch itself.
+bool paged_decode_supported(const PagedP& p, int32_t max_q);
+size_t paged_decode_workspace_bytes(size_t& zero);
+cudaError_t launch_paged_decode(const PagedP& p, void* ws, cudaStream_t st);
+
+}  // namespace attn

@@ -343,7 +343,8 @@ size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, 
  * ATTN_ERR_UNSUPPORTED. q's dtype is the cache's, or for an ATTN_E4M3 cache any
  * of the other three; o's is q's. Scores take the cached code times its
  * scale exactly (the scale multiplies the fp32 score, and the probability in
- * front of the value row). Infinities and NaN in rows a query does not see
+ * front of the value row; the tensor-core kernels round that probability to
+ * the cache's 16-bit type, to bf16 for an ATTN_E4M3 cache). Infinities and NaN in rows a query does not see
  * do not reach it. A row whose allowed scores are all -inf counts as empty.
  * max_q: the largest n_b, if the caller knows it, else 0: it chooses
  * between kernels and never changes which tokens are attended. The result is

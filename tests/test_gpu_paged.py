@@ -180,7 +180,7 @@ def one_case(kind, qd, cd, mask, *, heads_first=True, sink=False, max_q=True, se
     z = torch.randn(c["Hq"], generator=torch.Generator().manual_seed(seed)).cuda() if sink else None
     o, lse = run(q, cache, c["new"], allowed=allowed_of(mask, z), max_q=max(c["new"]) if max_q else 0)
     ref = reference(q, K, V, c["new"], c["lens"], c["d"] ** -0.5, sink=None if z is None else z.cpu(), **mask)
-    check(o, lse, *ref, tensor_core=qd != "f32")
+    check(o, lse, *ref, tensor_core=qd != "f32", cache=cd)
     return o, lse
 
 
@@ -226,12 +226,12 @@ def test_rows_outside_every_sequence_and_strides(kind, new, cd):
     eta.attn_paged_fwd(q, cache, cu, eta.AllowedSet(causal=True), out=o, lse=lse, workspace=ws, max_q=new)
     assert eta.attn_get_status(ws) == 0
     ref = reference(q[2:-3], K, V, [new] * B, lens, 128 ** -0.5)
-    check(o[2:-3], lse[2:-3], *ref, tensor_core=True)
+    check(o[2:-3], lse[2:-3], *ref, tensor_core=True, cache=cd)
     for part in (o[:2], o[-3:], lse[:2], lse[-3:]):
         assert (part == 5).all()
     # without cu_q: the same number each
     o2, lse2 = run(q[2:-3], cache, allowed=eta.AllowedSet(causal=True), max_q=new)
-    check(o2, lse2, *ref, tensor_core=True)
+    check(o2, lse2, *ref, tensor_core=True, cache=cd)
 
 
 @pytest.mark.parametrize("fmt", [(True, False), (False, True), (True, True)])
@@ -272,7 +272,7 @@ def test_empty_rows_and_bad_pages(kind, new, cd):
         assert torch.allclose(lse[:empty].cpu(), z.expand(empty, 4), rtol=2.0 ** -22, atol=0)
         t = reference(q[empty:], K[1:], V[1:], [min(new, 2), new], [2, 300], 128 ** -0.5,
                       sink=None if sink is None else sink.cpu(), skip=skip[1:])
-        check(o[empty:], lse[empty:], *t, tensor_core=True)
+        check(o[empty:], lse[empty:], *t, tensor_core=True, cache=cd)
 
 
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
@@ -392,7 +392,7 @@ def test_captured_step_replays_with_new_lengths(new):
                 dense[b][lens[b] - new:lens[b]] = c.double() * sc.double()[..., None]
         ref = reference(q, [k[:L] for k, L in zip(K, lens)], [v[:L] for v, L in zip(V, lens)], [new] * B, lens,
                         128 ** -0.5, window=200, first=4)
-        check(*out[t % 2], *ref, tensor_core=True)
+        check(*out[t % 2], *ref, tensor_core=True, cache=E4M3)
     assert eta.attn_get_status(ws) == 0
 
 
