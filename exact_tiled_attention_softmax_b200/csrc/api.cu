@@ -667,11 +667,15 @@ attn_status attn_cache_read(const attn_cache* cache, attn_tensor* k, attn_tensor
 }
 
 size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, const attn_mask* mask) {
-  (void)q;
-  (void)cache;
   (void)mask;
+  CacheP c;
+  if (!q || q->ndim != 3 || check_cache(cache, c) != ATTN_OK || !dims_fit_int(q) || q->shape[1] < 1 ||
+      q->shape[1] % c.Hkv || q->shape[0] * q->shape[1] >= kMaxRowWarps)
+    return kStatusBytes;
   size_t zero;
-  return kStatusBytes + paged_decode_workspace_bytes(zero);
+  const size_t decode = paged_decode_workspace_bytes(zero);
+  const size_t chunk = paged_chunk_workspace_bytes(q->shape[0], c.batch, (int)(q->shape[1] / c.Hkv));
+  return kStatusBytes + (decode > chunk ? decode : chunk);
 }
 
 attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn_cache* cache, const attn_mask* mask,
@@ -716,13 +720,17 @@ attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn
   p.scale = scale;
   const int64_t bound = max_q ? max_q : (cu_q || !p.c.batch ? rows : rows / p.c.batch);
   const bool decode = paged_decode_supported(p, (int32_t)(bound < rows ? bound : rows));
+  const bool none = !rows || !p.c.batch;
+  const bool chunk = !none && !decode && paged_chunk_supported(p);
   size_t zero = 0;
   if (decode) paged_decode_workspace_bytes(zero);
-  if (cudaMemsetAsync(workspace, 0, kStatusBytes + zero, cs) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (!rows || !p.c.batch) return ATTN_OK;
+  if (!chunk && cudaMemsetAsync(workspace, 0, kStatusBytes + zero, cs) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (none) return ATTN_OK;
+  char* scratch = static_cast<char*>(workspace) + kStatusBytes;
   main_kernel_begin(cs);
-  const cudaError_t e =
-      decode ? launch_paged_decode(p, static_cast<char*>(workspace) + kStatusBytes, cs) : launch_paged_rows(p, cs);
+  const cudaError_t e = decode  ? launch_paged_decode(p, scratch, cs)
+                        : chunk ? launch_paged_chunk(p, scratch, cs)
+                                : launch_paged_rows(p, cs);
   main_kernel_end(cs);
   return cuda_status(e);
 }

@@ -229,10 +229,11 @@ __device__ __forceinline__ void finish_four(const PagedP& p, const Item& it, int
 __device__ __forceinline__ float part_factor(float m, float M) { return m == M ? 1.f : exp2f(m - M); }
 
 // Joins `parts` results: part(i, r, m, l) and vec(i, r, c4) give the i-th one's
-// summary and four elements; put(r, c4, M, l, v) takes the sum. All threads.
+// summary and four elements; put(r, c4, M, l, v) takes the sum. By `threads`
+// threads, of which the caller is number tid.
 template <int kD, class Part, class Vec, class Put>
-__device__ __forceinline__ void join_parts(int rows, int parts, Part part, Vec vec, Put put) {
-  for (int e = threadIdx.x; e < rows * (kD / 4); e += blockDim.x) {
+__device__ __forceinline__ void join_parts(int tid, int threads, int rows, int parts, Part part, Vec vec, Put put) {
+  for (int e = tid; e < rows * (kD / 4); e += threads) {
     const int r = e / (kD / 4), c4 = e % (kD / 4);
     float M = -INFINITY;
     for (int i = 0; i < parts; ++i) {
@@ -278,7 +279,7 @@ __device__ __forceinline__ void split_join(const PagedP& p, const SplitP& sp, Sp
   __threadfence();
   auto at = [&](int i) { return split_slot<kRows, kD>(sp, c0 + i, i == 0 ? 1 : 0); };
   join_parts<kD>(
-      it.rows, c1 - c0 + 1,
+      threadIdx.x, blockDim.x, it.rows, c1 - c0 + 1,
       [&](int i, int r, float& m, float& l) {
         const float* x = at(i) + kRows * kD;
         m = __ldcg(x + r);
@@ -294,13 +295,13 @@ template <int kRows, int kD, bool kHalf, class Part, class Vec>
 __device__ __forceinline__ void split_finish(const PagedP& p, const SplitP& sp, SplitShared& ss, const Share& sh,
                                              const Item& it, int k0, int k1, int parts, Part part, Vec vec) {
   if (k0 == 0 && k1 == it.tiles) {
-    join_parts<kD>(it.rows, parts, part, vec, [&](int r, int c4, float M, float l, const float4& v) {
+    join_parts<kD>(threadIdx.x, blockDim.x, it.rows, parts, part, vec, [&](int r, int c4, float M, float l, const float4& v) {
       finish_four<kHalf>(p, it, r, c4, M, l, v);
     });
     return;
   }
   float* slot = split_slot<kRows, kD>(sp, blockIdx.x, k0 == 0 ? 1 : 0);
-  join_parts<kD>(it.rows, parts, part, vec, [&](int r, int c4, float M, float l, const float4& v) {
+  join_parts<kD>(threadIdx.x, blockDim.x, it.rows, parts, part, vec, [&](int r, int c4, float M, float l, const float4& v) {
     __stcg(reinterpret_cast<float4*>(slot) + r * (kD / 4) + c4, v);
     if (c4 == 0) {
       slot[kRows * kD + r] = M;

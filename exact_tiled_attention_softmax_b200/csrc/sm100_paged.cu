@@ -1,0 +1,1118 @@
+// Attention of chunks of new tokens over a paged cache on the tensor cores:
+// 16-bit or e4m3 cache, d = dv = 128, pages of a multiple of 16 positions.
+//
+// A block of query rows is up to 256 (token, head of the group) rows of one
+// K/V head, tokens outer, so that a K/V tile serves every query head that reads
+// it and a short chunk still fills the 128-row products. Two 128-row halves
+// with a softmax warpgroup each alternate on the tensor core, as in the dense
+// forward kernel: S = Q K^T into TMEM, one row per thread turned into P in
+// place, O += P V into TMEM.
+//
+// K/V tiles of 128 keys come page by page: each lane of the producer warp
+// looks up the page of one box of the tile and issues its copies; boxes past
+// the sequence's end or in a page outside the pool are copied from past the
+// tensor's edge, that is as zeros. An e4m3 tile lands in a raw buffer, and four
+// warps turn it into the 16-bit operand tile (exact), while the row scales stay
+// fp32: K's multiplies the score, V's the probability.
+//
+// A masked key's V row may hold anything, and 0 times an infinity is not 0.
+// In tiles that some row sees only in part the checker warps (e4m3: the
+// converting ones) therefore take non-finite elements of V out of the operand;
+// rows that do see such a key get them back in the epilogue, where the result is
+// not finite whatever the probability was.
+//
+// Work split: plan_kernel lists the blocks of every sequence, deals whole items
+// (block, K/V head) to the CTAs round by round, so that the CTAs walk the same
+// head's tiles in step and find them in L2, and cuts the tiles of the
+// remaining items into shares that even the CTAs out. An item in several
+// shares is joined by the CTA that finishes last, in share order.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "paged.cuh"
+#include "paged_split.cuh"
+#include "sm100_paged.h"
+#include "sm100_softmax.cuh"
+
+namespace attn {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kPD = 128;         // head width
+constexpr int kPTile = 128;      // keys per tile
+constexpr int kPRows = 256;      // query rows per block, two halves
+constexpr int kPStages = 2;      // K/V ring depth
+constexpr int kPMinTiles = 2;    // tiles a CTA takes at least
+constexpr uint32_t kPTileB = kPTile * kPD * 2;  // 32 KB
+constexpr uint32_t kPRawB = kPTile * kPD;       // 16 KB, e4m3
+constexpr uint32_t kPQ = 0;
+constexpr uint32_t kPK = kPQ + 2 * kPTileB;
+constexpr uint32_t kPV = kPK + kPStages * kPTileB;
+constexpr uint32_t kPRaw = kPV + kPStages * kPTileB;  // e4m3: K, V
+
+// ------------------------------------------------------------------- plan
+
+struct PlanHead {
+  int64_t total;                       // tiles of all items
+  int32_t pairs, items, rounds, ranks; // (sequence, block) pairs; items = pairs x Hkv; whole rounds; shares
+};
+struct PlanCta {
+  int64_t u, left;          // its share: `left` tiles from tile index u on
+  int32_t item, at, rank, pad;  // that is tile `at` of `item`; the share's number
+};
+struct PlanPair {
+  int32_t b, blk, tiles, pad;
+};
+
+struct PlanP {
+  PlanHead* head;
+  PlanCta* cta;       // [ctas]
+  int64_t* starts;    // [ctas] first tile of each share
+  int32_t* cta_of;    // [ctas] its CTA
+  PlanPair* pair;     // [cap] longest blocks of a sequence first
+  int64_t* prefix;    // [cap + 1] tiles before the pair's items
+  int32_t* first;     // [batch + 1] blocks before the sequence
+  uint32_t* counters; // [ctas]
+  float* part;        // [ctas][2] partial results
+  int32_t ctas, cap;
+  int32_t tokens;     // tokens per block
+};
+
+// Block blk of sequence b: its rows and the key tiles they see.
+__device__ __forceinline__ Item block_item(const PagedP& p, int tokens, int b, int blk) {
+  Item it;
+  it.b = b;
+  it.h = 0;
+  it.s = seq_view(p.c, b);
+  const int group = p.Hq / p.c.Hkv;
+  const int tok0 = blk * tokens, ntok = it.s.n - tok0 < tokens ? it.s.n - tok0 : tokens;
+  it.row0 = tok0 * group;
+  it.rows = ntok * group;
+  it.blocks = (it.s.n + tokens - 1) / tokens;
+  const int64_t p0 = it.s.L - it.s.n + tok0, p1 = p0 + ntok - 1;
+  const int64_t top = (p.flags & ATTN_MASK_CAUSAL) && p1 < it.s.L - 1 ? p1 : it.s.L - 1;
+  it.hi = top < 0 ? 0 : (int)(top / kPTile) + 1;
+  it.lo = it.nf = 0;
+  if (p.flags & ATTN_MASK_WINDOW) {
+    const int64_t lo = p0 - p.window + 1;
+    it.lo = lo > 0 ? (int)(lo / kPTile) : 0;
+    const int64_t f = p.first < top + 1 ? p.first : top + 1;
+    it.nf = f > 0 ? (int)((f + kPTile - 1) / kPTile) : 0;
+  }
+  const int from = it.lo > it.nf ? it.lo : it.nf;
+  it.tiles = it.nf + (it.hi > from ? it.hi - from : 0);
+  if (it.tiles < 1) it.tiles = 1;
+  return it;
+}
+
+// Largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
+template <typename T>
+__device__ __forceinline__ int last_at_most(const T* a, int n, T x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_plan() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP pl) {
+  __shared__ SplitShared ss;
+  __shared__ int64_t longest;
+  dependents_may_launch();
+  const CacheP& c = p.c;
+  const int tid = threadIdx.x, n = blockDim.x, B = c.batch, Hkv = c.Hkv, G = pl.ctas;
+  if (tid < (int)(kStatusBytes / 4)) c.status[tid] = 0u;
+  for (int i = tid; i < G; i += n) pl.counters[i] = 0u;
+  __syncthreads();
+  report_ragged(c);
+  int64_t before, carry = 0;
+  for (int b0 = 0; b0 < B; b0 += n) {
+    const int b = b0 + tid;
+    const int64_t blocks = b < B ? (seq_view(c, b).n + pl.tokens - 1) / pl.tokens : 0;
+    const int64_t sum = block_sum_scan(blocks, ss, before);
+    if (b < B) pl.first[b] = (int)(carry + before < pl.cap ? carry + before : pl.cap);
+    carry += sum;
+  }
+  // More blocks than cap only come from overlapping cu_q ranges (reported).
+  const int NB = (int)(carry < pl.cap ? carry : pl.cap);
+  __syncthreads();
+  carry = 0;
+  for (int j0 = 0; j0 < NB; j0 += n) {
+    const int j = j0 + tid;
+    int64_t units = 0;
+    if (j < NB) {
+      const int i = NB - 1 - j, b = last_at_most(pl.first, B, i), blk = i - pl.first[b];
+      const int tiles = block_item(p, pl.tokens, b, blk).tiles;
+      pl.pair[j] = PlanPair{b, blk, tiles, 0};
+      units = (int64_t)tiles * Hkv;
+    }
+    const int64_t sum = block_sum_scan(units, ss, before);
+    if (j < NB) pl.prefix[j] = carry + before;
+    carry += sum;
+  }
+  const int64_t W = carry;
+  if (tid == 0) pl.prefix[NB] = W;
+  __syncthreads();
+  const int NI = NB * Hkv;
+  // Whole rounds, as many as leave no CTA (much) longer than the average.
+  const int64_t avg = (W + G - 1) / G;
+  int rounds = NI / G;
+  int64_t whole = 0;
+  const int most = rounds;
+  for (int tries = 0; rounds > 0; ++tries) {
+    if (tid == 0) longest = 0;
+    __syncthreads();
+    whole = 0;
+    if (tid < G)
+      for (int r = 0; r < rounds; ++r) whole += pl.pair[(tid + r * G) / Hkv].tiles;
+    atomicMax(reinterpret_cast<unsigned long long*>(&longest), (unsigned long long)whole);
+    __syncthreads();
+    const bool fits = longest * 32 <= avg * 33;
+    __syncthreads();
+    if (fits) break;
+    rounds = tries == 0 ? rounds - 1 : tries == 1 ? most * 3 / 4 : tries == 2 ? most / 2 : 0;
+  }
+  if (rounds == 0) whole = 0;
+  const int F = rounds * G;
+  const int64_t u0 = F < NI ? pl.prefix[F / Hkv] + (int64_t)(F % Hkv) * pl.pair[F / Hkv].tiles : W;
+  const int64_t rest = W - u0;
+  int64_t active = (rest + kPMinTiles - 1) / kPMinTiles;
+  active = active > G ? G : active;
+  const int64_t need = tid >= G ? 0 : rounds ? (avg > whole ? avg - whole : 0) : (tid < active ? 1 : 0);
+  int64_t total = block_sum_scan(need, ss, before);
+  if (total < 1) total = 1;
+  const int64_t u = u0 + before * rest / total, end = u0 + (before + need) * rest / total;
+  const bool has = tid < G && end > u;
+  int64_t rank;
+  const int64_t ranks = block_sum_scan(has ? 1 : 0, ss, rank);
+  if (tid < G) {
+    PlanCta t{u, has ? end - u : 0, 0, 0, (int)rank, 0};
+    if (has) {
+      const int j = last_at_most(pl.prefix, NB, u), tiles = pl.pair[j].tiles;
+      const int64_t rem = u - pl.prefix[j];
+      t.item = j * Hkv + (int)(rem / tiles);
+      t.at = (int)(rem % tiles);
+      pl.starts[rank] = u;
+      pl.cta_of[rank] = tid;
+    }
+    pl.cta[tid] = t;
+  }
+  if (tid == 0) *pl.head = PlanHead{W, NB, NI, rounds, (int)ranks};
+}
+
+// The pieces of one CTA in order; every role of the CTA walks the same ones.
+struct Pieces {
+  PlanHead head;
+  PlanCta mine;
+  int r;
+  __device__ __forceinline__ void init(const PlanP& pl) {
+    head = *pl.head;
+    mine = pl.cta[blockIdx.x];
+    r = 0;
+  }
+  // The next piece: item it, tiles [k0, k1); u: index of its first tile, -1 in a whole round.
+  __device__ __forceinline__ bool next(const PagedP& p, const PlanP& pl, Item& it, int& k0, int& k1, int64_t& u) {
+    int item;
+    if (r < head.rounds) {
+      item = blockIdx.x + r * pl.ctas;
+      ++r;
+      u = -1;
+    } else if (mine.left > 0) {
+      item = mine.item;
+      u = mine.u;
+    } else {
+      return false;
+    }
+    const PlanPair pr = pl.pair[item / p.c.Hkv];
+    it = block_item(p, pl.tokens, pr.b, pr.blk);
+    it.h = item % p.c.Hkv;
+    if (u < 0) {
+      k0 = 0;
+      k1 = it.tiles;
+    } else {
+      k0 = mine.at;
+      k1 = it.tiles - k0 < mine.left ? it.tiles : (int)(k0 + mine.left);
+      mine.left -= k1 - k0;
+      mine.u += k1 - k0;
+      mine.item++;
+      mine.at = 0;
+    }
+    return true;
+  }
+};
+
+// What the two halves of a block see of a tile.
+struct Halves {
+  int rows[2];
+  int64_t p0[2], p1[2];  // positions of the half's first and last token
+  int64_t L, window, first;
+  bool causal, win;
+  __device__ __forceinline__ void init(const PagedP& p, const Item& it) {
+    const int group = p.Hq / p.c.Hkv;
+    const int64_t base = it.s.L - it.s.n;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      rows[w] = it.rows - 128 * w;
+      rows[w] = rows[w] < 0 ? 0 : (rows[w] > 128 ? 128 : rows[w]);
+      p0[w] = base + (it.row0 + 128 * w) / group;
+      p1[w] = base + (it.row0 + 128 * w + rows[w] - 1) / group;
+    }
+    L = it.s.L;
+    causal = p.flags & ATTN_MASK_CAUSAL;
+    win = p.flags & ATTN_MASK_WINDOW;
+    window = p.window;
+    first = p.first;
+  }
+  // kEmptyH: no row of half w sees a key of tile kt; kFullH: all see all.
+  __device__ __forceinline__ int cls(int w, int kt) const {
+    const int64_t c0 = (int64_t)kt * kPTile, c1 = c0 + kPTile - 1;
+    if (rows[w] == 0 || c0 >= L || p1[w] < 0) return 0;
+    if (causal && c0 > p1[w]) return 0;
+    if (win && c0 >= first && c1 <= p0[w] - window) return 0;
+    if (c1 >= L || p0[w] < 0 || (causal && c1 > p0[w])) return 1;
+    if (win && c1 >= first && (c0 > first ? c0 : first) <= p1[w] - window) return 1;
+    return 2;
+  }
+  // Bits 2 w, 2 w + 1: the class of half w.
+  __device__ __forceinline__ uint32_t both(int kt) const { return (uint32_t)cls(0, kt) | (uint32_t)cls(1, kt) << 2; }
+};
+
+// Some half sees the tile in part.
+__device__ __forceinline__ bool in_part(uint32_t cls) { return (cls & 3u) == 1u || (cls >> 2) == 1u; }
+
+// First k in [k, k1) whose tile some half sees (k1 when none), and its classes.
+__device__ __forceinline__ int next_seen(const Item& it, const Halves& hv, int k, int k1, uint32_t& cls) {
+  for (; k < k1; ++k)
+    if ((cls = hv.both(it.tile_at(k))) != 0u) return k;
+  cls = 0;
+  return k1;
+}
+
+struct PagedCtl {
+  uint64_t q_full;
+  uint64_t raw_full[2], raw_empty[2];  // e4m3: raw K, raw V
+  uint64_t k_full[kPStages], v_full[kPStages], v_ok[kPStages], kv_empty[kPStages];
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_final;
+  uint64_t join;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+  uint32_t odd_piece;  // 1 + the piece whose V tiles lost non-finite elements
+  int32_t last;
+  // Per stage: bits 0-3 the halves' classes, bit 4 another tile follows, bits
+  // 8-15 boxes in pages outside the pool. raw_info: the same, with the raw K tile.
+  uint32_t tinfo[kPStages];
+  uint32_t raw_info;
+};
+
+template <bool kQ8>
+struct PagedSmem {
+  static constexpr uint32_t kScale = kPRaw + (kQ8 ? 2 * kPRawB : 0);  // kPStages x (128 K, 128 V) fp32
+  static constexpr uint32_t kCtl = kScale + (kQ8 ? kPStages * 1024 : 0);
+  static constexpr uint32_t kBytes = kCtl + 512;
+  static constexpr int kThreads = kQ8 ? 448 : 384;
+  static constexpr int kCheckers = kQ8 ? 4 : 2;  // warps 2, 3 (and 12, 13)
+};
+static_assert(sizeof(PagedCtl) <= 512, "control block");
+
+// Row i's keys of tile kt as two 64-bit words.
+__device__ __forceinline__ void row_bits(const Halves& hv, int64_t pos, bool live, int kt, uint32_t bad, int box,
+                                         uint64_t& w0, uint64_t& w1) {
+  const int64_t j0 = (int64_t)kt * kPTile;
+  w0 = w1 = 0ull;
+  if (!live || pos < 0) return;
+  int64_t hi = hv.L - 1;
+  if (hv.causal && pos < hi) hi = pos;
+  int64_t lo = j0;
+  if (hv.win && pos - hv.window + 1 > lo) lo = pos - hv.window + 1;
+  w0 = range_bits64(lo - j0, hi - j0);
+  w1 = range_bits64(lo - j0 - 64, hi - j0 - 64);
+  if (hv.win && j0 < hv.first) {
+    const int64_t fh = hv.first - 1 < hi ? hv.first - 1 : hi;
+    w0 |= range_bits64(0, fh - j0);
+    w1 |= range_bits64(-64, fh - j0 - 64);
+  }
+  while (bad) {
+    const int i = __ffs(bad) - 1;
+    bad &= bad - 1;
+    w0 &= ~range_bits64(i * box, i * box + box - 1);
+    w1 &= ~range_bits64(i * box - 64, i * box + box - 65);
+  }
+}
+
+// The row of an e4m3 tile: scores times the keys' scales (which carry
+// c log2(e)), probabilities times the V rows' scales before they are rounded.
+// Like the 16-bit rows' functions otherwise, with their strict rules.
+template <bool kMasked>
+__device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* ksc, const float* vsc, uint64_t mw0,
+                                                     uint64_t mw1, float& m_run, float& l_run) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    uint32_t r[32];
+    tmem_ld32(tS + q * 32, r);
+    tmem_wait_ld();
+    const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const float4 k4 = *reinterpret_cast<const float4*>(ksc + q * 32 + e);
+      float x0 = __uint_as_float(r[e]) * k4.x, x1 = __uint_as_float(r[e + 1]) * k4.y;
+      float x2 = __uint_as_float(r[e + 2]) * k4.z, x3 = __uint_as_float(r[e + 3]) * k4.w;
+      if constexpr (kMasked) {
+        x0 = (mw >> e) & 1u ? x0 : -INFINITY;
+        x1 = (mw >> (e + 1)) & 1u ? x1 : -INFINITY;
+        x2 = (mw >> (e + 2)) & 1u ? x2 : -INFINITY;
+        x3 = (mw >> (e + 3)) & 1u ? x3 : -INFINITY;
+      }
+      a = max3nan(a, x0, x1);
+      b = max3nan(b, x2, x3);
+    }
+    mx = max3nan(mx, a, b);
+  }
+  const bool poison = !(mx < INFINITY);
+  if (poison) mx = -INFINITY;
+  const float alpha = move_max(mx, m_run);
+  const float msub = m_run == -INFINITY ? 0.f : m_run;
+  const uint64_t nm2 = f2_pack(-msub, -msub);
+  uint64_t acc0 = 0ull, acc1 = 0ull;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    uint32_t r[32];
+    tmem_ld32(tS + q * 32, r);
+    tmem_wait_ld();
+    const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const float4 k4 = *reinterpret_cast<const float4*>(ksc + q * 32 + e);
+      const float4 v4 = *reinterpret_cast<const float4*>(vsc + q * 32 + e);
+      float x[4], y[4];
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), f2_pack(k4.x, k4.y), nm2), x[0], x[1]);
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), f2_pack(k4.z, k4.w), nm2), x[2],
+                x[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = !kMasked || ((mw >> (e + i)) & 1u) ? ex2(x[i]) : 0.f;
+      acc0 = f2_add(acc0, f2_pack(y[0], y[1]));
+      acc1 = f2_add(acc1, f2_pack(y[2], y[3]));
+      float z[4] = {y[0] * v4.x, y[1] * v4.y, y[2] * v4.z, y[3] * v4.w};
+      if constexpr (kMasked) {  // a masked row's scale may hold anything
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = (mw >> (e + i)) & 1u ? z[i] : 0.f;
+      }
+      pk[e / 2] = pack_bf16(z[0], z[1]);
+      pk[e / 2 + 1] = pack_bf16(z[2], z[3]);
+    }
+    tmem_st16(tS + q * 16, pk);
+  }
+  float a0, a1, b0, b1;
+  f2_unpack(acc0, a0, a1);
+  f2_unpack(acc1, b0, b1);
+  l_run = poison ? NAN : l_run * alpha + ((a0 + a1) + (b0 + b1));
+  return alpha;
+}
+
+__device__ __forceinline__ float ldf16(const uint16_t* p, bool f16) {
+  const uint16_t v = *p;
+  return f16 ? __half2float(*reinterpret_cast<const __half*>(&v)) : __uint_as_float((uint32_t)v << 16);
+}
+
+template <bool v>
+struct Tag {
+  static constexpr bool value = v;
+};
+
+template <bool kH, bool kQ8>
+__global__ void __launch_bounds__(PagedSmem<kQ8>::kThreads, 1)
+paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PagedP p,
+                   const PlanP pl, int box) {
+  using M = PagedSmem<kQ8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  PagedCtl* ctl = reinterpret_cast<PagedCtl*>(smem + M::kCtl);
+  volatile uint32_t* abort_flag = &ctl->abort_flag;
+  const CacheP& c = p.c;
+  uint32_t* status = c.status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr bool kHP = kH && !kQ8;  // P and V in fp16, else bf16
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&ctl->q_full), 8);
+    for (int s = 0; s < kPStages; ++s) {
+      mbar_init(smem_u32(&ctl->raw_full[s]), 1);
+      mbar_init(smem_u32(&ctl->raw_empty[s]), M::kCheckers);
+      mbar_init(smem_u32(&ctl->k_full[s]), kQ8 ? M::kCheckers : 1);
+      mbar_init(smem_u32(&ctl->v_full[s]), 1);
+      mbar_init(smem_u32(&ctl->v_ok[s]), M::kCheckers);
+      mbar_init(smem_u32(&ctl->kv_empty[s]), 1);
+      mbar_init(smem_u32(&ctl->s_full[s]), 1);
+      mbar_init(smem_u32(&ctl->p_full[s]), 4);
+    }
+    mbar_init(smem_u32(&ctl->o_final), 1);
+    mbar_init(smem_u32(&ctl->join), 8);
+    ctl->abort_flag = 0;
+    ctl->odd_piece = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  // TMEM columns: S/P of half w at 128 w, O of half w at 256 + 128 w.
+  wait_for_plan();
+  Pieces pieces;
+  pieces.init(pl);
+  Item it;
+  Halves hv;
+  int k0, k1;
+  int64_t u;
+
+  if (warp == 0) {
+    // ---------------- producer: lane i < 128 / box takes box i of every tile
+    if (lane == 0) {
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+    }
+    const int boxes = kPTile / box;
+    int n = 0;
+    bool ok = true;
+    while (ok && pieces.next(p, pl, it, k0, k1, u)) {
+      hv.init(p, it);
+      uint32_t cls;
+      int k = next_seen(it, hv, k0, k1, cls);
+      auto page_at = [&](int kk) {  // -2: past the end, -1: outside the pool
+        const int64_t j = (int64_t)it.tile_at(kk) * kPTile + lane * box;
+        if (lane >= boxes || j >= it.s.L) return -2;
+        return (int)page_of(c, it.b, j);
+      };
+      int pg = k < k1 ? page_at(k) : -2;
+      while (k < k1) {
+        uint32_t ncls;
+        const int nk = next_seen(it, hv, k + 1, k1, ncls);
+        const int npg = nk < k1 ? page_at(nk) : -2;
+        const int s = n % kPStages;
+        const uint32_t info = cls | (nk < k1 ? 16u : 0u) | __ballot_sync(0xffffffffu, pg == -1) << 8;
+        const int off = (int)(((int64_t)it.tile_at(k) * kPTile + lane * box) % c.page_size);
+        const int page = pg < 0 ? c.num_pages : pg;
+        if constexpr (!kQ8) {
+          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl->kv_empty[s]), ((n / kPStages) & 1) ^ 1, abort_flag, status));
+          if (!ok) break;
+          const uint32_t kf = smem_u32(&ctl->k_full[s]), vf = smem_u32(&ctl->v_full[s]);
+          if (lane == 0) {
+            ctl->tinfo[s] = info;  // published by the arrive below
+            mbar_expect_tx(kf, kPTileB);
+            mbar_expect_tx(vf, kPTileB);
+          }
+          __syncwarp();
+          if (lane < boxes) {
+            const uint32_t kd = sbase + kPK + s * kPTileB + lane * box * 128;
+            const uint32_t vd = sbase + kPV + s * kPTileB + lane * box * 128;
+            tma_load_4d(kd, &tk, kf, 0, off, it.h, page);
+            tma_load_4d(kd + kPTileB / 2, &tk, kf, 64, off, it.h, page);
+            tma_load_4d(vd, &tv, vf, 0, off, it.h, page);
+            tma_load_4d(vd + kPTileB / 2, &tv, vf, 64, off, it.h, page);
+          }
+        } else {
+          const uint32_t kf = smem_u32(&ctl->raw_full[0]), vf = smem_u32(&ctl->raw_full[1]);
+          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl->raw_empty[0]), (n & 1) ^ 1, abort_flag, status));
+          if (!ok) break;
+          if (lane == 0) {
+            ctl->raw_info = info;
+            mbar_expect_tx(kf, kPRawB);
+          }
+          __syncwarp();
+          if (lane < boxes) tma_load_4d(sbase + kPRaw + lane * box * 128, &tk, kf, 0, off, it.h, page);
+          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl->raw_empty[1]), (n & 1) ^ 1, abort_flag, status));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(vf, kPRawB);
+          __syncwarp();
+          if (lane < boxes) tma_load_4d(sbase + kPRaw + kPRawB + lane * box * 128, &tv, vf, 0, off, it.h, page);
+        }
+        __syncwarp();
+        ++n;
+        k = nk;
+        cls = ncls;
+        pg = npg;
+      }
+    }
+    // Every copy lands before the CTA's shared memory goes.
+    if constexpr (!kQ8) {
+      for (int r = (n > kPStages ? n - kPStages : 0); r < n; ++r) {
+        wait_bar(smem_u32(&ctl->k_full[r % kPStages]), (r / kPStages) & 1, abort_flag, nullptr);
+        wait_bar(smem_u32(&ctl->v_full[r % kPStages]), (r / kPStages) & 1, abort_flag, nullptr);
+      }
+    } else if (n > 0) {
+      wait_bar(smem_u32(&ctl->raw_full[0]), (n - 1) & 1, abort_flag, nullptr);
+      wait_bar(smem_u32(&ctl->raw_full[1]), (n - 1) & 1, abort_flag, nullptr);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (whole warp; one elected lane issues)
+    const bool leader = elect_one();
+    constexpr uint32_t idS = idesc16<kH>(128, 128, 0, 0);
+    constexpr uint32_t idPV = idesc16<kHP>(128, 128, 0, 1);
+    const uint64_t dQ0 = smem_desc_sw128(sbase + kPQ, 16, 1024), dK0 = smem_desc_sw128(sbase + kPK, 16, 1024);
+    const uint64_t dV0 = smem_desc_sw128(sbase + kPV, kPTileB / 2, 1024);
+    constexpr uint64_t kTileStep = kPTileB >> 4;
+    auto wait_all = [&](uint64_t* bar, uint32_t par) {
+      return __all_sync(0xffffffffu, wait_bar(smem_u32(bar), par, abort_flag, status));
+    };
+    auto issue_s = [&](int w, int stage) {
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((kk >> 2) * (kPTileB / 2) + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + w * 128, dQ0 + (uint64_t)w * kTileStep + off, dK0 + (uint64_t)stage * kTileStep + off, idS, kk > 0);
+        }
+        mma_commit(smem_u32(&ctl->s_full[w]));
+      }
+      __syncwarp();
+    };
+    int n = 0, piece = 0;
+    int done[2] = {0, 0};  // P tiles taken of each half, over all pieces
+    bool ok = true;
+    while (ok && pieces.next(p, pl, it, k0, k1, u)) {
+      hv.init(p, it);
+      uint32_t cls;
+      const bool any = next_seen(it, hv, k0, k1, cls) < k1;
+      if (!(ok = wait_all(&ctl->q_full, piece & 1))) break;
+      tc_fence_after();
+      uint32_t info = 0;
+      int npv[2] = {0, 0};
+      if (any) {
+        const int s = n % kPStages;
+        if (!(ok = wait_all(&ctl->k_full[s], (n / kPStages) & 1))) break;
+        tc_fence_after();
+        info = ctl->tinfo[s];
+        for (int w = 0; w < 2; ++w)
+          if ((info >> (2 * w)) & 3u) issue_s(w, s);
+      }
+      while (any) {
+        const int s = n % kPStages, s1 = (n + 1) % kPStages;
+        const bool more = info & 16u;
+        uint32_t ninfo = 0;
+        for (int w = 0; w < 2 && ok; ++w) {
+          if ((info >> (2 * w)) & 3u) {
+            if (!(ok = wait_all(&ctl->p_full[w], done[w] & 1))) break;
+            if (!(ok = wait_all(&ctl->v_ok[s], (n / kPStages) & 1))) break;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8,
+                       dV0 + (uint64_t)s * kTileStep + (uint64_t)(kk * (2048 >> 4)), idPV,
+                       (npv[w] > 0 || kk > 0) ? 1u : 0u);
+            }
+            __syncwarp();
+            ++npv[w];
+            ++done[w];
+          }
+          if (more) {
+            if (w == 0) {
+              if (!(ok = wait_all(&ctl->k_full[s1], ((n + 1) / kPStages) & 1))) break;
+              tc_fence_after();
+              ninfo = ctl->tinfo[s1];
+            }
+            if ((ninfo >> (2 * w)) & 3u) issue_s(w, s1);
+          }
+        }
+        if (!ok) break;
+        if (leader) mma_commit(smem_u32(&ctl->kv_empty[s]));
+        __syncwarp();
+        ++n;
+        if (!more) break;
+        info = ninfo;
+      }
+      if (!ok) break;
+      if (leader) mma_commit(smem_u32(&ctl->o_final));
+      __syncwarp();
+      ++piece;
+    }
+  } else if (warp < 4 || warp >= 12) {
+    // ---------------- checkers (e4m3: converters): V's non-finite elements, and
+    // an e4m3 tile's 16-bit form
+    const int ci = warp < 4 ? warp - 2 : warp - 10;
+    int n = 0, piece = 0;
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t par) {
+      return __all_sync(0xffffffffu, wait_bar(smem_u32(bar), par, abort_flag, status));
+    };
+    while (ok && pieces.next(p, pl, it, k0, k1, u)) {
+      hv.init(p, it);
+      uint32_t cls;
+      float ks_next = 0.f, vs_next = 0.f;
+      // e4m3: thread row of the tile, and its scales one tile ahead.
+      const int row = ci * 32 + lane;
+      auto scales = [&](int kk) {
+        const int64_t j = (int64_t)it.tile_at(kk) * kPTile + row;
+        ks_next = vs_next = 0.f;
+        if (j >= it.s.L) return;
+        const int64_t pg = c.table[(int64_t)it.b * c.table_stride + j / c.page_size], o = j % c.page_size;
+        if (pg < 0 || pg >= c.num_pages) return;
+        ks_next = c.ks[pg * c.sks[0] + o * c.sks[1] + (int64_t)it.h * c.sks[2]] * (p.scale * kLog2e);
+        vs_next = c.vs[pg * c.svs[0] + o * c.svs[1] + (int64_t)it.h * c.svs[2]];
+      };
+      int k = next_seen(it, hv, k0, k1, cls);
+      if constexpr (kQ8)
+        if (k < k1) scales(k);
+      while (k < k1) {
+        const int s = n % kPStages;
+        const uint32_t par = (n / kPStages) & 1;
+        const int64_t live = it.s.L - (int64_t)it.tile_at(k) * kPTile;  // rows of the tile inside the sequence
+        const bool part = in_part(cls);
+        uint32_t ncls;
+        const int nk = next_seen(it, hv, k + 1, k1, ncls);
+        bool odd = false;
+        if constexpr (!kQ8) {
+          if (!(ok = wait_all(&ctl->v_full[s], par))) break;
+          if (part) {
+            const uint32_t expo = kHP ? 0x7c00u : 0x7f80u;
+            const uint32_t base = kPV + s * kPTileB + ci * (kPTileB / 2);  // one 64-column half a warp
+#pragma unroll 4
+            for (int i = 0; i < (int)(kPTileB / 2 / 512); ++i) {
+              uint4* at = reinterpret_cast<uint4*>(smem + base + i * 512 + lane * 16);
+              uint4 v = *at;
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              bool hit = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & expo) == expo) {
+                  w[e] &= 0xffff0000u;
+                  hit = true;
+                }
+                if (((w[e] >> 16) & expo) == expo) {
+                  w[e] &= 0x0000ffffu;
+                  hit = true;
+                }
+              }
+              if (hit) {
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+                odd = odd || i * 4 + (lane >> 3) < live;
+              }
+            }
+            fence_proxy_async_smem();
+          }
+        } else {
+          const float ks = ks_next, vs = vs_next;
+          if (nk < k1) scales(nk);
+          // K: wait for the raw tile and for the operand stage
+          if (!(ok = wait_all(&ctl->raw_full[0], n & 1))) break;
+          if (!(ok = wait_all(&ctl->kv_empty[s], par ^ 1))) break;
+          if (ci == 0 && lane == 0) ctl->tinfo[s] = ctl->raw_info;
+          float* sc = reinterpret_cast<float*>(smem + M::kScale + s * 1024);
+          sc[row] = ks;
+          sc[128 + row] = vs;
+          auto turn = [&](auto to_fp16, uint32_t raw, uint32_t dst, bool clean) {
+            constexpr bool kOutH = decltype(to_fp16)::value;
+#pragma unroll 2
+            for (int ch = 0; ch < 8; ++ch) {  // 16 codes -> two 16-byte chunks
+              const uint4 v = *reinterpret_cast<const uint4*>(smem + raw + sw128_offset(row, ch * 16));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t x = w[e];
+                if (clean) {
+                  // codes 0x7f and 0xff (NaN) to 0
+                  const uint32_t nan = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                  if (nan) {
+                    x &= ~((nan >> 7) * 0xffu);
+                    odd = odd || row < live;
+                  }
+                }
+                uint32_t h0, h1;
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+                    "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+                    : "=r"(h0), "=r"(h1)
+                    : "r"(x));
+                if constexpr (kOutH) {
+                  o[2 * e] = h0;
+                  o[2 * e + 1] = h1;
+                } else {
+                  const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
+                  o[2 * e] = pack_bf16(f0.x, f0.y);
+                  o[2 * e + 1] = pack_bf16(f1.x, f1.y);
+                }
+              }
+              const uint32_t half = dst + (ch >> 2) * (kPTileB / 2);
+              *reinterpret_cast<uint4*>(smem + half + sw128_offset(row, (ch & 3) * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(smem + half + sw128_offset(row, (ch & 3) * 32 + 16)) =
+                  make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          };
+          turn(Tag<kH>(), kPRaw, kPK + s * kPTileB, false);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&ctl->k_full[s]));
+            mbar_arrive(smem_u32(&ctl->raw_empty[0]));
+          }
+          if (!(ok = wait_all(&ctl->raw_full[1], n & 1))) break;
+          turn(Tag<false>(), kPRaw + kPRawB, kPV + s * kPTileB, part);
+          fence_proxy_async_smem();
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+          // Rare. The mark is set while this piece's rows are being worked on:
+          // after their Q came, before the last of this tile's products.
+          if (!(ok = wait_all(&ctl->q_full, piece & 1))) break;
+          if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&ctl->odd_piece) = (uint32_t)piece + 1u;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ctl->v_ok[s]));
+          if constexpr (kQ8) mbar_arrive(smem_u32(&ctl->raw_empty[1]));
+        }
+        ++n;
+        k = nk;
+        cls = ncls;
+      }
+      ++piece;
+    }
+  } else {
+    // ---------------- softmax warpgroups: warps 4-7 and 8-11, thread t of
+    // warpgroup w owns row 128 w + t of the block (TMEM lane t).
+    const int w = (warp - 4) >> 2;
+    const int t = ((warp & 3) << 5) | lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + w * 128, tO = tmem + lane_off + 256 + w * 128;
+    const int group = p.Hq / c.Hkv;
+    int n = 0, mine = 0, piece = 0;
+    uint32_t joins = 0;
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t par) {
+      return __all_sync(0xffffffffu, wait_bar(smem_u32(bar), par, abort_flag, status));
+    };
+    auto both_groups = [&]() {  // the 256 softmax threads meet (a bounded wait)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->join));
+      return wait_all(&ctl->join, joins++ & 1);
+    };
+    while (ok && pieces.next(p, pl, it, k0, k1, u)) {
+      hv.init(p, it);
+      // ---- Q: a half-warp a row, 16 bytes a lane; rows past the block's are zero.
+      // Every product of the previous piece has completed (o_final).
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = (warp & 3) * 32 + 2 * i + (lane >> 4), rr = 128 * w + r;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < it.rows) {
+          int64_t tok;
+          int h;
+          row_place(p, it, rr, tok, h);
+          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + tok * p.sq[0] + h * p.sq[1] +
+                                              (lane & 15) * 8);
+        }
+        const uint32_t dst = kPQ + w * kPTileB + ((lane >> 3) & 1) * (kPTileB / 2) + sw128_offset(r, (lane & 7) * 16);
+        *reinterpret_cast<uint4*>(smem + dst) = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full));
+
+      const int rr = 128 * w + t;
+      const bool valid = rr < it.rows;
+      const int64_t pos = it.s.L - it.s.n + (it.row0 + rr) / group;
+      float m_run = -INFINITY, l_run = 0.f;
+      int got = 0;
+      uint32_t cls;
+      for (int k = next_seen(it, hv, k0, k1, cls); k < k1; k = next_seen(it, hv, k + 1, k1, cls), ++n) {
+        const uint32_t cl = (cls >> (2 * w)) & 3u;
+        if (cl == 0u) continue;
+        const int kt = it.tile_at(k), s = n % kPStages;
+        if (!(ok = wait_all(&ctl->s_full[w], mine & 1))) break;
+        tc_fence_after();
+        const uint32_t bad = (ctl->tinfo[s] >> 8) & 0xffu;
+        uint64_t w0 = ~0ull, w1 = ~0ull;
+        const bool full = cl == 2u && bad == 0u;
+        if (!full) row_bits(hv, pos, valid, kt, bad, box, w0, w1);
+        float alpha;
+        if constexpr (!kQ8) {
+          const float sl2 = p.scale * kLog2e;
+          alpha = full ? softmax_full_tile<kH, false, true>(tS, sl2, m_run, l_run, ~0ull, ~0ull)
+                       : softmax_masked_tile<kH, true>(tS, sl2, w0, w1, ~0ull, ~0ull, m_run, l_run);
+        } else {
+          const float* sc = reinterpret_cast<const float*>(smem + M::kScale + s * 1024);
+          alpha = full ? softmax_scaled_tile<false>(tS, sc, sc + 128, w0, w1, m_run, l_run)
+                       : softmax_scaled_tile<true>(tS, sc, sc + 128, w0, w1, m_run, l_run);
+        }
+        if (got > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t o[32];
+            tmem_ld32(tO + ch * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + ch * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[w]));
+        ++got;
+        ++mine;
+      }
+      if (!ok || !(ok = wait_all(&ctl->o_final, piece & 1))) break;
+      tc_fence_after();
+      // ---- epilogue: the rows, or this piece's part of them
+      const bool whole = k0 == 0 && k1 == it.tiles;
+      const bool odd = *reinterpret_cast<volatile uint32_t*>(&ctl->odd_piece) == (uint32_t)piece + 1u;
+      int64_t tok;
+      int h;
+      row_place(p, it, valid ? rr : 0, tok, h);
+      float lse = 0.f, osc = 1.f;
+      if (whole) osc = finish_scale(p, h, m_run, l_run, lse);
+      uint16_t* orow = static_cast<uint16_t*>(p.o) + tok * p.so[0] + h * p.so[1];
+      float* slot = split_slot<kPRows, kPD>(SplitP{0, 0, nullptr, pl.part}, blockIdx.x, k0 == 0 ? 1 : 0);
+#pragma unroll 1
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t o[32];
+        if (got > 0) {
+          tmem_ld32(tO + ch * 32, o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (got == 0 || l_run == 0.f) o[e] = 0u;
+        if (odd) {  // non-finite V elements that the checkers took out, of the keys that this row sees
+          uint32_t c2;
+#pragma unroll 1
+          for (int k = next_seen(it, hv, k0, k1, c2); k < k1; k = next_seen(it, hv, k + 1, k1, c2)) {
+            if (!in_part(c2)) continue;
+            const int kt = it.tile_at(k);
+            uint64_t w0, w1;
+            row_bits(hv, pos, valid, kt, 0u, box, w0, w1);
+#pragma unroll 1
+            for (int j = 0; j < kPTile; ++j) {
+              if (!(((j < 64 ? w0 : w1) >> (j & 63)) & 1ull)) continue;
+              const int64_t key = (int64_t)kt * kPTile + j;
+              const int64_t pg = page_of(c, it.b, key);
+              if (pg < 0) continue;
+              const int64_t at = pg * c.sv[0] + key % c.page_size * c.sv[1] + (int64_t)it.h * c.sv[2] + ch * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float v = kQ8 ? ld(static_cast<const __nv_fp8_e4m3*>(c.v) + at + e)
+                                    : ldf16(static_cast<const uint16_t*>(c.v) + at + e, kH);
+                if (!isfinite(v)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
+              }
+            }
+          }
+        }
+        if (valid && whole) {
+#pragma unroll
+          for (int c8 = 0; c8 < 4; ++c8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              pk[e] = pack16<kH>(__uint_as_float(o[c8 * 8 + 2 * e]) * osc, __uint_as_float(o[c8 * 8 + 2 * e + 1]) * osc);
+            *reinterpret_cast<uint4*>(orow + ch * 32 + c8 * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int c4 = 0; c4 < 8; ++c4)
+            __stcg(reinterpret_cast<uint4*>(slot + (size_t)rr * kPD + ch * 32) + c4,
+                   make_uint4(o[4 * c4], o[4 * c4 + 1], o[4 * c4 + 2], o[4 * c4 + 3]));
+        }
+      }
+      if (valid && whole) p.lse[tok * p.sl[0] + h * p.sl[1]] = lse;
+      if (!whole) {
+        if (valid) {
+          slot[kPRows * kPD + rr] = m_run;
+          slot[kPRows * kPD + kPRows + rr] = l_run;
+        }
+        // ---- count the piece; the last one joins them all, in share order
+        const int64_t first = u - k0;
+        const int r1 = pieces.mine.rank;
+        const int r0 = last_at_most(pl.starts, r1 + 1, first);
+        const int rl = last_at_most(pl.starts, pieces.head.ranks, first + it.tiles - 1);
+        __threadfence();
+        if (!(ok = both_groups())) break;
+        if (w == 0 && t == 0) ctl->last = atomicAdd(pl.counters + r0, 1u) == (uint32_t)(rl - r0);
+        if (!(ok = both_groups())) break;
+        if (*reinterpret_cast<volatile int32_t*>(&ctl->last)) {
+          __threadfence();
+          auto at = [&](int i) {
+            const int cta = pl.cta_of[r0 + i];
+            return split_slot<kPRows, kPD>(SplitP{0, 0, nullptr, pl.part}, cta, i == 0 ? 1 : 0);
+          };
+          join_parts<kPD>(
+              threadIdx.x - 128, 256, it.rows, rl - r0 + 1,
+              [&](int i, int r, float& m, float& l) {
+                const float* x = at(i) + kPRows * kPD;
+                m = __ldcg(x + r);
+                l = __ldcg(x + kPRows + r);
+              },
+              [&](int i, int r, int c4) { return __ldcg(reinterpret_cast<const float4*>(at(i)) + r * (kPD / 4) + c4); },
+              [&](int r, int c4, float mm, float l, const float4& v) { finish_four<kH>(p, it, r, c4, mm, l, v); });
+        }
+      }
+      tc_fence_before();
+      ++piece;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------------- host helpers
+
+PFN_cuTensorMapEncodeTiled_v12000 paged_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }
+  return fn;
+}
+
+// 4-D map over (d, position in page, head, page) with a (64 or 128, box, 1, 1)
+// box of 128-byte rows, 128-byte swizzle.
+bool pool_map(CUtensorMap* map, const void* base, const CacheP& c, const int64_t s[3], int box) {
+  auto fn = paged_encode_fn();
+  if (!fn) return false;
+  const bool q8 = c.dtype == ATTN_E4M3;
+  const cuuint64_t el = q8 ? 1 : 2;
+  cuuint64_t dims[4] = {(cuuint64_t)kPD, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)s[1] * el, (cuuint64_t)s[2] * el, (cuuint64_t)s[0] * el};
+  cuuint32_t bx[4] = {q8 ? 128u : 64u, (cuuint32_t)box, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  const auto type = q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                       : c.dtype == ATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(map, type, 4, const_cast<void*>(base), dims, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Keys per copy box: the largest power of two up to 128 that divides the page.
+int box_of(int page_size) {
+  int b = 16;
+  while (b < kPTile && page_size % (2 * b) == 0) b *= 2;
+  return b;
+}
+
+struct PlanSizes {
+  size_t head, cta, starts, cta_of, pair, prefix, first, counters, part, total;
+  int cap;
+};
+
+PlanSizes plan_sizes(int64_t rows, int batch, int group) {
+  PlanSizes z;
+  const int tokens = kPRows / group, G = sm_count();
+  z.cap = (int)(rows / tokens + batch);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t a = at;
+    at += align_up(bytes, 256);
+    return a;
+  };
+  z.head = take(sizeof(PlanHead));
+  z.cta = take(sizeof(PlanCta) * G);
+  z.starts = take(sizeof(int64_t) * (G + 1));
+  z.cta_of = take(sizeof(int32_t) * G);
+  z.pair = take(sizeof(PlanPair) * z.cap);
+  z.prefix = take(sizeof(int64_t) * (z.cap + 1));
+  z.first = take(sizeof(int32_t) * (batch + 1));
+  z.counters = take(sizeof(uint32_t) * G);
+  z.part = take(sizeof(float) * split_part_floats<kPRows, kPD>() * 2 * G);
+  z.total = at;
+  return z;
+}
+
+template <bool kH, bool kQ8>
+cudaError_t launch_chunk(const PagedP& p, const PlanP& pl, const CUtensorMap& mk, const CUtensorMap& mv, int box,
+                         cudaStream_t st) {
+  using M = PagedSmem<kQ8>;
+  auto kern = paged_chunk_kernel<kH, kQ8>;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)M::kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = true;
+  }
+  plan_kernel<<<1, 1024, 0, st>>>(p, pl);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // The chunk kernel's set-up runs under the plan; it waits for the plan's end
+  // before it reads anything.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pl.ctas);
+  cfg.blockDim = dim3(M::kThreads);
+  cfg.dynamicSmemBytes = M::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mk, mv, p, pl, box);
+}
+
+}  // namespace
+
+bool paged_chunk_supported(const PagedP& p) {
+  if (!paged_pieces_ok(p) || p.Hq / p.c.Hkv > kPRows || sm_count() > 1024 || !paged_encode_fn()) return false;
+  const CacheP& c = p.c;
+  // What a tensor map can describe: positive strides below 2^40 bytes.
+  for (int i = 0; i < 3; ++i)
+    if (c.sk[i] < 1 || c.sv[i] < 1 || c.sk[i] >= (1LL << 38) || c.sv[i] >= (1LL << 38)) return false;
+  int dev = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  return major == 10 && minor == 0;
+}
+
+size_t paged_chunk_workspace_bytes(int64_t rows, int batch, int group) {
+  return group > kPRows ? 0 : plan_sizes(rows, batch, group).total;
+}
+
+cudaError_t launch_paged_chunk(const PagedP& p, void* ws, cudaStream_t st) {
+  const CacheP& c = p.c;
+  const PlanSizes z = plan_sizes(c.rows, c.batch, p.Hq / c.Hkv);
+  char* w = static_cast<char*>(ws);
+  PlanP pl;
+  pl.head = reinterpret_cast<PlanHead*>(w + z.head);
+  pl.cta = reinterpret_cast<PlanCta*>(w + z.cta);
+  pl.starts = reinterpret_cast<int64_t*>(w + z.starts);
+  pl.cta_of = reinterpret_cast<int32_t*>(w + z.cta_of);
+  pl.pair = reinterpret_cast<PlanPair*>(w + z.pair);
+  pl.prefix = reinterpret_cast<int64_t*>(w + z.prefix);
+  pl.first = reinterpret_cast<int32_t*>(w + z.first);
+  pl.counters = reinterpret_cast<uint32_t*>(w + z.counters);
+  pl.part = reinterpret_cast<float*>(w + z.part);
+  pl.ctas = sm_count();
+  pl.cap = z.cap;
+  pl.tokens = kPRows / (p.Hq / c.Hkv);
+  const int box = box_of(c.page_size);
+  CUtensorMap mk, mv;
+  if (!pool_map(&mk, c.k, c, c.sk, box) || !pool_map(&mv, c.v, c, c.sv, box)) return cudaErrorInvalidValue;
+  const bool h = p.dtype == ATTN_F16;
+  if (c.dtype == ATTN_E4M3)
+    return h ? launch_chunk<true, true>(p, pl, mk, mv, box, st) : launch_chunk<false, true>(p, pl, mk, mv, box, st);
+  return h ? launch_chunk<true, false>(p, pl, mk, mv, box, st) : launch_chunk<false, false>(p, pl, mk, mv, box, st);
+}
+
+}  // namespace attn

@@ -17,4 +17,12 @@ bool paged_decode_supported(const PagedP& p, int32_t max_q);
 size_t paged_decode_workspace_bytes(size_t& zero);
 cudaError_t launch_paged_decode(const PagedP& p, void* ws, cudaStream_t st);
 
+// Any number of new tokens: 256-row blocks on tcgen05. Its plan kernel clears
+// the status word and everything else that must start at zero. Workspace
+// bytes after the status block, for `rows` new tokens in `batch` sequences and
+// `group` query heads per K/V head.
+bool paged_chunk_supported(const PagedP& p);
+size_t paged_chunk_workspace_bytes(int64_t rows, int batch, int group);
+cudaError_t launch_paged_chunk(const PagedP& p, void* ws, cudaStream_t st);
+
 }  // namespace attn

@@ -327,6 +327,18 @@ __device__ __forceinline__ float min3f(float a, float b, float c) {
   return r;
 }
 
+// The same, NaN if any operand is (max.f32 drops a NaN).
+__device__ __forceinline__ float max3nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Two fp32 lanes in one 64-bit register, for the packed f32x2 FMA path.
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
   uint64_t r;
