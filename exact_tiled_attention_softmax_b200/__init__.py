@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -149,20 +150,26 @@ _DTYPES = {torch.float32: ATTN_F32, torch.bfloat16: ATTN_BF16, torch.float16: AT
            torch.float8_e4m3fn: ATTN_E4M3}
 
 
-def _fill(c: AttnTensorC, t: torch.Tensor) -> AttnTensorC:
-    if t.dim() > 4:
+# attn_tensor and attn_cache as packed bytes: filling a ctypes structure field
+# by field costs several microseconds a tensor, more than a small kernel runs.
+_TENSOR = struct.Struct("@Pii4q4q")
+_CACHE = struct.Struct("@" + 4 * "Pii4q4q" + "PqiiP")
+assert _TENSOR.size == ctypes.sizeof(AttnTensorC) and _CACHE.size == ctypes.sizeof(AttnCacheC)
+_PAD = tuple((0,) * (4 - n) for n in range(5))
+_NO_TENSOR = (0,) * 11
+
+
+def _fields(t: torch.Tensor) -> tuple:
+    """attn_tensor's fields for t, in order."""
+    n = t.dim()
+    if n > 4:
         raise ValueError("at most 4 dimensions")
-    c.data = t.data_ptr() if t.numel() else 0
-    c.dtype = _DTYPES.get(t.dtype, -1)
-    c.ndim = t.dim()
-    for i in range(t.dim()):
-        c.shape[i] = t.shape[i]
-        c.stride[i] = t.stride(i)
-    return c
+    pad = _PAD[n]
+    return (t.data_ptr() if t.numel() else 0, _DTYPES.get(t.dtype, -1), n, *t.shape, *pad, *t.stride(), *pad)
 
 
 def _tensor(t: torch.Tensor | None):
-    return None if t is None else _fill(AttnTensorC(), t)
+    return None if t is None else AttnTensorC.from_buffer_copy(_TENSOR.pack(*_fields(t)))
 
 
 def _ref(c):
@@ -284,18 +291,22 @@ class AllowedSet:
             m.starts_stride_b = st.stride(0) if st.dim() == 2 and st.shape[0] > 1 else 0
         if self.sink is not None:
             m.sink = self.sink.data_ptr()
-        m.lse_format = (ATTN_LSE_KV_ONLY if self.lse_kv_only else 0) | \
-            (ATTN_LSE_NEG_LOG2 if self.lse_neg_log2 else 0)
-        m.bwd_flags = ATTN_BWD_DETERMINISTIC if self.deterministic else 0
-        m.dropout_p = float(self.dropout_p)
-        m.dropout_seed = int(self.dropout_seed) & 0xFFFFFFFFFFFFFFFF
+        if self.lse_kv_only or self.lse_neg_log2:
+            m.lse_format = (ATTN_LSE_KV_ONLY if self.lse_kv_only else 0) | \
+                (ATTN_LSE_NEG_LOG2 if self.lse_neg_log2 else 0)
+        if self.deterministic:
+            m.bwd_flags = ATTN_BWD_DETERMINISTIC
+        if self.dropout_p or self.dropout_seed:
+            m.dropout_p = float(self.dropout_p)
+            m.dropout_seed = int(self.dropout_seed) & 0xFFFFFFFFFFFFFFFF
         m.flags = flags
         return m
 
 
 def _stream_handle(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:  # torch's current stream of the current device, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -474,22 +485,18 @@ class PagedCache:
 
     def to_c(self) -> AttnCacheC:
         """The C descriptor, after the checks that raw pointers cannot carry."""
-        _check_mask_tensor(self.block_table, "block_table", (torch.int32,), (2,))
-        _check_mask_tensor(self.seq_lens, "seq_lens", (torch.int32,), (1,))
-        if self.block_table.shape[0] != self.seq_lens.shape[0]:
+        table, lens = self.block_table, self.seq_lens
+        _check_mask_tensor(table, "block_table", (torch.int32,), (2,))
+        _check_mask_tensor(lens, "seq_lens", (torch.int32,), (1,))
+        B, pages = table.shape
+        if B != lens.shape[0]:
             raise ValueError("block_table and seq_lens hold different numbers of sequences")
-        _check_on(self.k.device, *self.tensors())
-        c = AttnCacheC()
-        _fill(c.k, self.k)
-        _fill(c.v, self.v)
-        if self.k_scale is not None:
-            _fill(c.k_scale, self.k_scale)
-        if self.v_scale is not None:
-            _fill(c.v_scale, self.v_scale)
-        c.batch, c.max_pages = self.block_table.shape
-        c.block_table, c.table_stride = self.block_table.data_ptr(), self.block_table.stride(0)
-        c.seq_lens = self.seq_lens.data_ptr()
-        return c
+        _check_on(self.k.device, self.v, table, lens, self.k_scale, self.v_scale)
+        return AttnCacheC.from_buffer_copy(_CACHE.pack(
+            *_fields(self.k), *_fields(self.v),
+            *(_NO_TENSOR if self.k_scale is None else _fields(self.k_scale)),
+            *(_NO_TENSOR if self.v_scale is None else _fields(self.v_scale)),
+            table.data_ptr(), table.stride(0), pages, B, lens.data_ptr()))
 
 
 def _cu_q_ptr(cu_q, cache: PagedCache):
@@ -505,10 +512,10 @@ def _cu_q_ptr(cu_q, cache: PagedCache):
 def _launch_on(device: torch.device, call, stream) -> int:
     """call(stream handle) with `device` current: the library launches on the
     current device, and the default stream is that device's current one."""
-    if device.index == torch.cuda.current_device():
-        return call(_stream_handle(stream))
-    with torch.cuda.device(device):
-        return call(_stream_handle(stream))
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call(_stream_handle(stream))
+    return call(_stream_handle(stream))
 
 
 def _workspace_args(workspace) -> tuple:
@@ -583,9 +590,13 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
 
     def call(s):
         ws = workspace
-        if ws is None:  # from the launching stream's pool: freed here, reused there after the call
-            with torch.cuda.stream(stream):
-                ws = _workspace(lib.attn_paged_workspace_size(_ref(cq), _ref(c), _ref(m)), q.device)
+        if ws is None:
+            need = lib.attn_paged_workspace_size(_ref(cq), _ref(c), _ref(m))
+            if stream is None:
+                ws = _workspace(need, q.device)
+            else:  # from that stream's pool: freed here, reused there after the call
+                with torch.cuda.stream(stream):
+                    ws = _workspace(need, q.device)
         return lib.attn_paged_fwd(_ref(cq), cu, _ref(c), _ref(m), ctypes.c_float(scale), int(max_q), _ref(co),
                                   _ref(cl), *_workspace_args(ws), s)
 

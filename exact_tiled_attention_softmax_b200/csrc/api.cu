@@ -199,6 +199,10 @@ attn_status check_pool(const attn_tensor* t, int ndim, const int64_t* shape, boo
   return reinterpret_cast<uintptr_t>(t->data) % elem_bytes(t->dtype) ? ATTN_ERR_INVALID_ARG : ATTN_OK;
 }
 
+// Positions, windows and new tokens stay below 2^30, so that the kernels' 32-bit
+// differences of them cannot overflow.
+constexpr int64_t kMaxPositions = 1LL << 30;
+
 // The cache descriptor's host-side checks, and the kernels' form of it.
 attn_status check_cache(const attn_cache* c, CacheP& p) {
   if (!c || c->k.ndim != 4 || c->v.ndim != 4 || !dims_fit_int(&c->k) || !dims_fit_int(&c->v))
@@ -227,7 +231,7 @@ attn_status check_cache(const attn_cache* c, CacheP& p) {
   }
   if (c->batch < 0 || c->max_pages < 0 || (c->batch > 1 && c->table_stride < c->max_pages)) return ATTN_ERR_INVALID_ARG;
   if (c->batch && (!c->seq_lens || (c->max_pages && !c->block_table))) return ATTN_ERR_INVALID_ARG;
-  if ((int64_t)c->max_pages * p.page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if ((int64_t)c->max_pages * p.page_size > kMaxPositions) return ATTN_ERR_UNSUPPORTED;
   p.k = c->k.data;
   p.v = c->v.data;
   for (int i = 0; i < 3; ++i) {
@@ -248,6 +252,7 @@ attn_status check_cache(const attn_cache* c, CacheP& p) {
 // Rows of new tokens: every sequence's share must be whole when cu_q is NULL.
 attn_status check_rows(int64_t rows, const int32_t* cu_q, CacheP& p) {
   if (!cu_q && (p.batch ? rows % p.batch : rows) != 0) return ATTN_ERR_INVALID_ARG;
+  if (rows > kMaxPositions) return ATTN_ERR_UNSUPPORTED;
   p.cu_q = cu_q;
   p.rows = (int32_t)rows;
   return ATTN_OK;
@@ -713,13 +718,14 @@ attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn
   p.dtype = q->dtype;
   const MaskP m = mask_params(mask);
   p.flags = m.flags;
-  p.window = m.window < 0x7fffffff ? m.window : 0x7fffffff;
-  p.first = m.first;
+  p.window = m.window < kMaxPositions ? m.window : kMaxPositions;
+  p.first = m.first < kMaxPositions ? m.first : kMaxPositions;
   p.sink = m.sink;
   p.lse_fmt = m.lse_fmt;
   p.scale = scale;
   const int64_t bound = max_q ? max_q : (cu_q || !p.c.batch ? rows : rows / p.c.batch);
-  const bool decode = paged_decode_supported(p, (int32_t)(bound < rows ? bound : rows));
+  const int32_t longest = (int32_t)(bound < rows ? bound : rows);
+  const bool decode = paged_decode_supported(p, longest);
   const bool none = !rows || !p.c.batch;
   const bool chunk = !none && !decode && paged_chunk_supported(p);
   size_t zero = 0;
@@ -728,7 +734,7 @@ attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn
   if (none) return ATTN_OK;
   char* scratch = static_cast<char*>(workspace) + kStatusBytes;
   main_kernel_begin(cs);
-  const cudaError_t e = decode  ? launch_paged_decode(p, scratch, cs)
+  const cudaError_t e = decode  ? launch_paged_decode(p, longest, scratch, cs)
                         : chunk ? launch_paged_chunk(p, scratch, cs)
                                 : launch_paged_rows(p, cs);
   main_kernel_end(cs);

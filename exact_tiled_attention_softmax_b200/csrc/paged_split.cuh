@@ -236,6 +236,7 @@ __device__ __forceinline__ void join_parts(int tid, int threads, int rows, int p
   for (int e = tid; e < rows * (kD / 4); e += threads) {
     const int r = e / (kD / 4), c4 = e % (kD / 4);
     float M = -INFINITY;
+#pragma unroll 8
     for (int i = 0; i < parts; ++i) {
       float m, l;
       part(i, r, m, l);
@@ -243,6 +244,7 @@ __device__ __forceinline__ void join_parts(int tid, int threads, int rows, int p
     }
     float L = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int i = 0; i < parts; ++i) {
       float m, l;
       part(i, r, m, l);

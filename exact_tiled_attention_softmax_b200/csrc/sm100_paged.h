@@ -15,7 +15,7 @@ bool paged_pieces_ok(const PagedP& p);
 // launch itself.
 bool paged_decode_supported(const PagedP& p, int32_t max_q);
 size_t paged_decode_workspace_bytes(size_t& zero);
-cudaError_t launch_paged_decode(const PagedP& p, void* ws, cudaStream_t st);
+cudaError_t launch_paged_decode(const PagedP& p, int32_t max_q, void* ws, cudaStream_t st);
 
 // Any number of new tokens: 256-row blocks on tcgen05. Its plan kernel clears
 // the status word and everything else that must start at zero. Workspace

@@ -320,7 +320,9 @@ typedef struct attn_cache {
  * throughout. A page position must be written by one token only: pages
  * shared between sequences hold whichever token was stored last.
  * workspace: NULL (device checks are then applied but not reported), or at
- * least 256 bytes for the status word. */
+ * least 256 bytes for the status word. Caches of more than 2^30 positions a
+ * sequence (max_pages * page_size), or more new tokens than that, are
+ * ATTN_ERR_UNSUPPORTED in all three calls. */
 attn_status attn_cache_write(const attn_tensor* k, const attn_tensor* v, const int32_t* cu_q,
                              const attn_cache* cache, void* workspace, size_t workspace_bytes, void* stream);
 
