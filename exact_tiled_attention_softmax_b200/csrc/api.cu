@@ -677,8 +677,7 @@ size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, 
   if (!q || q->ndim != 3 || check_cache(cache, c) != ATTN_OK || !dims_fit_int(q) || q->shape[1] < 1 ||
       q->shape[1] % c.Hkv || q->shape[0] * q->shape[1] >= kMaxRowWarps)
     return kStatusBytes;
-  size_t zero;
-  const size_t decode = paged_decode_workspace_bytes(zero);
+  const size_t decode = paged_decode_workspace_bytes();
   const size_t chunk = paged_chunk_workspace_bytes(q->shape[0], c.batch, (int)(q->shape[1] / c.Hkv));
   return kStatusBytes + (decode > chunk ? decode : chunk);
 }
@@ -725,12 +724,11 @@ attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn
   p.scale = scale;
   const int64_t bound = max_q ? max_q : (cu_q || !p.c.batch ? rows : rows / p.c.batch);
   const int32_t longest = (int32_t)(bound < rows ? bound : rows);
-  const bool decode = paged_decode_supported(p, longest);
   const bool none = !rows || !p.c.batch;
+  const bool decode = !none && paged_decode_supported(p, longest);
   const bool chunk = !none && !decode && paged_chunk_supported(p);
-  size_t zero = 0;
-  if (decode) paged_decode_workspace_bytes(zero);
-  if (!chunk && cudaMemsetAsync(workspace, 0, kStatusBytes + zero, cs) != cudaSuccess) return ATTN_ERR_CUDA;
+  if ((none || !(decode || chunk)) && cudaMemsetAsync(workspace, 0, kStatusBytes, cs) != cudaSuccess)
+    return ATTN_ERR_CUDA;
   if (none) return ATTN_OK;
   char* scratch = static_cast<char*>(workspace) + kStatusBytes;
   main_kernel_begin(cs);

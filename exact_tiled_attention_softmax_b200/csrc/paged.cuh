@@ -74,8 +74,8 @@ __device__ __forceinline__ SeqView seq_view(const CacheP& c, int b) {
 
 // Reports cu_q and seq_lens entries that seq_view clamps, or whose new tokens
 // do not fit their sequence. For one block of a launch, all threads.
-__device__ __forceinline__ void report_ragged(const CacheP& c) {
-  if (!c.status) return;
+__device__ __forceinline__ void report_ragged(const CacheP& c, uint32_t* status) {
+  if (!status) return;
   const int64_t cap = (int64_t)c.max_pages * c.page_size;
   bool bad = false;
   for (int b = threadIdx.x; b < c.batch; b += blockDim.x) {
@@ -83,8 +83,9 @@ __device__ __forceinline__ void report_ragged(const CacheP& c) {
     const int64_t lo = c.cu_q ? c.cu_q[b] : 0, hi = c.cu_q ? c.cu_q[b + 1] : (c.rows / c.batch);
     bad = bad || L < 0 || L > cap || lo < 0 || hi < lo || hi > c.rows || hi - lo > L;
   }
-  if (bad) set_status(c.status, ATTN_DEVERR_RAGGED);
+  if (bad) set_status(status, ATTN_DEVERR_RAGGED);
 }
+__device__ __forceinline__ void report_ragged(const CacheP& c) { report_ragged(c, c.status); }
 
 // The sequence that holds new token t, found by the whole (converged) warp:
 // the number of sequences that end at or before t. -1 when none does.

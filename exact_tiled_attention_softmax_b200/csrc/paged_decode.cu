@@ -149,7 +149,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 }
 
 template <int kMode, int kNT>
-__global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_decode_kernel(const PagedP p, const SplitP sp) {
+__global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_decode_kernel(const __grid_constant__ PagedP p,
+                                                                                       const __grid_constant__ SplitP sp) {
   using R = Ring<kMode, kNT>;
   constexpr bool kQ8 = R::kQ8;
   constexpr int kRows = 8 * kNT;
@@ -160,7 +161,14 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
   const CacheP& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3, g8 = lane >> 2;
   const uint32_t ring = smem_u32(smem) + warp * R::kWarpB;
-  if (blockIdx.x == 0) report_ragged(c);
+  // Errors gather in shared memory and leave with the CTA's record, so that
+  // nothing has to be cleared before the launch.
+  if (threadIdx.x == 0) {
+    ss.errors = 0u;
+    sp.rec[blockIdx.x].parts = 0;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) report_ragged(c, &ss.errors);
   const int group = p.Hq / c.Hkv;
   const bool causal = p.flags & ATTN_MASK_CAUSAL, window = p.flags & ATTN_MASK_WINDOW;
   const int W = (int)p.window, first = (int)p.first;
@@ -210,7 +218,7 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
             off_mine = j - e * c.page_size;
             pg_mine = c.table[(int64_t)it.b * c.table_stride + e];
             if (pg_mine < 0 || pg_mine >= c.num_pages) {
-              set_status(c.status, ATTN_DEVERR_PAGE);
+              atomicOr(&ss.errors, ATTN_DEVERR_PAGE);
               pg_mine = -1;
             }
           }
@@ -569,11 +577,20 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
     auto warp_vec = [&](int w, int r, int c4) {
       return reinterpret_cast<const float4*>(smem + w * R::kWarpB)[r * (kDD / 4) + c4];
     };
-    split_finish<kRows, kDD, kMode == kF16 || kMode == kE4m3F16>(p, sp, ss, share, it, k0, k1, kDWarps, warp_part,
-                                                                warp_vec);
+    split_finish<kRows, kDD, kMode == kF16 || kMode == kE4m3F16>(p, sp, share, it, k0, k1, kDWarps, warp_part, warp_vec);
     split_advance<kDTile, kRows>(p, share, it, k1 - k0);
     __syncthreads();  // the rings are free again
   }
+  __syncthreads();
+  if (threadIdx.x == 0) sp.rec[blockIdx.x].errors = ss.errors;
+}
+
+template <int kRows, bool kHalf>
+__global__ void __launch_bounds__(kJoinRows * 32) decode_join_kernel(const PagedP p, const SplitP sp) {
+  wait_for_previous();
+  join_record<kRows, kDD, kHalf>(p, sp.rec, sp.ctas, true, [&](int i, int e) {
+    return split_slot<kRows, kDD>(sp, i + e, e == 0 ? 1 : 0);
+  });
 }
 
 // Dynamic shared memory above the default, once per device and kernel.
@@ -591,7 +608,9 @@ cudaError_t launch_mode(const PagedP& p, SplitP sp, cudaStream_t st) {
   }
   sp.ctas = R::kCtas * sm_count();
   paged_decode_kernel<kMode, kNT><<<sp.ctas, kDThreads, R::kSmem, st>>>(p, sp);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_after(decode_join_kernel<8 * kNT, kMode == kF16 || kMode == kE4m3F16>, dim3(sp.ctas, kNT),
+                      kJoinRows * 32, 0, st, p, sp);
 }
 
 template <int kMode>
@@ -628,20 +647,18 @@ bool paged_decode_supported(const PagedP& p, int32_t max_q) {
   return paged_pieces_ok(p) && (int64_t)max_q * (p.Hq / p.c.Hkv) <= kMaxRows;
 }
 
-size_t paged_decode_workspace_bytes(size_t& zero) {
+size_t paged_decode_workspace_bytes() {
   const size_t ctas = (size_t)kMostCtas * sm_count();
-  zero = align_up(ctas * sizeof(uint32_t), 256);
-  return zero + ctas * 2 * split_part_floats<kMaxRows, kDD>() * sizeof(float);
+  return align_up(ctas * sizeof(JoinRec), 256) + ctas * 2 * split_part_floats<kMaxRows, kDD>() * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedP& p, int32_t max_q, void* ws, cudaStream_t st) {
-  size_t zero;
-  paged_decode_workspace_bytes(zero);
   SplitP sp;
   sp.ctas = 0;
   sp.min_tiles = kMinTiles;
-  sp.counters = static_cast<uint32_t*>(ws);
-  sp.part = reinterpret_cast<float*>(static_cast<char*>(ws) + zero);
+  sp.rec = static_cast<JoinRec*>(ws);
+  sp.part = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                     align_up((size_t)kMostCtas * sm_count() * sizeof(JoinRec), 256));
   const int rows = max_q * (p.Hq / p.c.Hkv);
   if (p.c.dtype == ATTN_E4M3)
     return p.dtype == ATTN_F16 ? launch_rows<kE4m3F16>(p, rows, sp, st) : launch_rows<kE4m3Bf16>(p, rows, sp, st);

@@ -75,7 +75,7 @@ struct PlanP {
   PlanPair* pair;     // [cap] longest blocks of a sequence first
   int64_t* prefix;    // [cap + 1] tiles before the pair's items
   int32_t* first;     // [batch + 1] blocks before the sequence
-  uint32_t* counters; // [ctas]
+  JoinRec* rec;       // [ctas] by share
   float* part;        // [ctas][2] partial results
   int32_t ctas, cap;
   int32_t tokens;     // tokens per block
@@ -122,9 +122,6 @@ __device__ __forceinline__ int last_at_most(const T* a, int n, T x) {
   return lo;
 }
 
-__device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_plan() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP pl) {
   __shared__ SplitShared ss;
   __shared__ int64_t longest;
@@ -132,7 +129,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP 
   const CacheP& c = p.c;
   const int tid = threadIdx.x, n = blockDim.x, B = c.batch, Hkv = c.Hkv, G = pl.ctas;
   if (tid < (int)(kStatusBytes / 4)) c.status[tid] = 0u;
-  for (int i = tid; i < G; i += n) pl.counters[i] = 0u;
+  for (int i = tid; i < G; i += n) pl.rec[i].parts = 0;
   __syncthreads();
   report_ragged(c);
   int64_t before, carry = 0;
@@ -304,11 +301,9 @@ struct PagedCtl {
   uint64_t k_full[kPStages], v_full[kPStages], v_ok[kPStages], kv_empty[kPStages];
   uint64_t s_full[2], p_full[2];
   uint64_t o_final;
-  uint64_t join;
   uint32_t tmem_base;
   uint32_t abort_flag;
   uint32_t odd_piece;  // 1 + the piece whose V tiles lost non-finite elements
-  int32_t last;
   // Per stage: bits 0-3 the halves' classes, bit 4 another tile follows, bits
   // 8-15 boxes in pages outside the pool. raw_info: the same, with the raw K tile.
   uint32_t tinfo[kPStages];
@@ -320,8 +315,8 @@ struct PagedSmem {
   static constexpr uint32_t kScale = kPRaw + (kQ8 ? 2 * kPRawB : 0);  // kPStages x (128 K, 128 V) fp32
   static constexpr uint32_t kCtl = kScale + (kQ8 ? kPStages * 1024 : 0);
   static constexpr uint32_t kBytes = kCtl + 512;
-  static constexpr int kThreads = kQ8 ? 448 : 384;
-  static constexpr int kCheckers = kQ8 ? 4 : 2;  // warps 2, 3 (and 12, 13)
+  static constexpr int kThreads = kQ8 ? 512 : 384;
+  static constexpr int kCheckers = kQ8 ? 4 : 2;  // warps 12-15, or 2 and 3
 };
 static_assert(sizeof(PagedCtl) <= 512, "control block");
 
@@ -434,8 +429,8 @@ struct Tag {
 
 template <bool kH, bool kQ8>
 __global__ void __launch_bounds__(PagedSmem<kQ8>::kThreads, 1)
-paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PagedP p,
-                   const PlanP pl, int box) {
+paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                   const __grid_constant__ PagedP p, const __grid_constant__ PlanP pl, int box) {
   using M = PagedSmem<kQ8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -459,7 +454,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
       mbar_init(smem_u32(&ctl->p_full[s]), 4);
     }
     mbar_init(smem_u32(&ctl->o_final), 1);
-    mbar_init(smem_u32(&ctl->join), 8);
     ctl->abort_flag = 0;
     ctl->odd_piece = 0;
     fence_barrier_init();
@@ -473,7 +467,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   // TMEM columns: S/P of half w at 128 w, O of half w at 256 + 128 w.
-  wait_for_plan();
+  wait_for_previous();
+  if constexpr (kQ8) {
+    // 512 threads start with 128 registers each; the softmax warpgroups take
+    // 160 of what the others leave (2 x 96 + 2 x 160 = 4 x 128).
+    if (warp < 4 || warp >= 12)
+      setmaxnreg_dec<96>();
+    else
+      setmaxnreg_inc<160>();
+  }
   Pieces pieces;
   pieces.init(pl);
   Item it;
@@ -641,10 +643,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
       __syncwarp();
       ++piece;
     }
-  } else if (warp < 4 || warp >= 12) {
+  } else if (kQ8 ? warp >= 12 : warp < 4) {
     // ---------------- checkers (e4m3: converters): V's non-finite elements, and
     // an e4m3 tile's 16-bit form
-    const int ci = warp < 4 ? warp - 2 : warp - 10;
+    const int ci = kQ8 ? warp - 12 : warp - 2;
     int n = 0, piece = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t par) {
@@ -781,7 +783,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
       }
       ++piece;
     }
-  } else {
+  } else if (warp >= 4) {
     // ---------------- softmax warpgroups: warps 4-7 and 8-11, thread t of
     // warpgroup w owns row 128 w + t of the block (TMEM lane t).
     const int w = (warp - 4) >> 2;
@@ -790,15 +792,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     const uint32_t tS = tmem + lane_off + w * 128, tO = tmem + lane_off + 256 + w * 128;
     const int group = p.Hq / c.Hkv;
     int n = 0, mine = 0, piece = 0;
-    uint32_t joins = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, wait_bar(smem_u32(bar), par, abort_flag, status));
-    };
-    auto both_groups = [&]() {  // the 256 softmax threads meet (a bounded wait)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->join));
-      return wait_all(&ctl->join, joins++ & 1);
     };
     while (ok && pieces.next(p, pl, it, k0, k1, u)) {
       hv.init(p, it);
@@ -934,30 +930,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
           slot[kPRows * kPD + rr] = m_run;
           slot[kPRows * kPD + kPRows + rr] = l_run;
         }
-        // ---- count the piece; the last one joins them all, in share order
-        const int64_t first = u - k0;
-        const int r1 = pieces.mine.rank;
-        const int r0 = last_at_most(pl.starts, r1 + 1, first);
-        const int rl = last_at_most(pl.starts, pieces.head.ranks, first + it.tiles - 1);
-        __threadfence();
-        if (!(ok = both_groups())) break;
-        if (w == 0 && t == 0) ctl->last = atomicAdd(pl.counters + r0, 1u) == (uint32_t)(rl - r0);
-        if (!(ok = both_groups())) break;
-        if (*reinterpret_cast<volatile int32_t*>(&ctl->last)) {
-          __threadfence();
-          auto at = [&](int i) {
-            const int cta = pl.cta_of[r0 + i];
-            return split_slot<kPRows, kPD>(SplitP{0, 0, nullptr, pl.part}, cta, i == 0 ? 1 : 0);
-          };
-          join_parts<kPD>(
-              threadIdx.x - 128, 256, it.rows, rl - r0 + 1,
-              [&](int i, int r, float& m, float& l) {
-                const float* x = at(i) + kPRows * kPD;
-                m = __ldcg(x + r);
-                l = __ldcg(x + kPRows + r);
-              },
-              [&](int i, int r, int c4) { return __ldcg(reinterpret_cast<const float4*>(at(i)) + r * (kPD / 4) + c4); },
-              [&](int r, int c4, float mm, float l, const float4& v) { finish_four<kH>(p, it, r, c4, mm, l, v); });
+        if (k0 == 0 && w == 0 && t == 0) {
+          const int last = last_at_most(pl.starts, pieces.head.ranks, u + it.tiles - 1);
+          JoinRec rec{last - pieces.mine.rank + 1, it.s.q0, it.row0, it.rows, it.h, 0u, {0, 0}};
+          pl.rec[pieces.mine.rank] = rec;
         }
       }
       tc_fence_before();
@@ -970,6 +946,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+template <bool kH>
+__global__ void __launch_bounds__(kJoinRows * 32) chunk_join_kernel(const PagedP p, const PlanP pl) {
+  wait_for_previous();
+  join_record<kPRows, kPD, kH>(p, pl.rec, pl.ctas, false, [&](int i, int e) {
+    return split_slot<kPRows, kPD>(SplitP{0, 0, nullptr, pl.part}, pl.cta_of[i + e], e == 0 ? 1 : 0);
+  });
 }
 
 // ----------------------------------------------------------- host helpers
@@ -1012,7 +996,7 @@ int box_of(int page_size) {
 }
 
 struct PlanSizes {
-  size_t head, cta, starts, cta_of, pair, prefix, first, counters, part, total;
+  size_t head, cta, starts, cta_of, pair, prefix, first, rec, part, total;
   int cap;
 };
 
@@ -1033,7 +1017,7 @@ PlanSizes plan_sizes(int64_t rows, int batch, int group) {
   z.pair = take(sizeof(PlanPair) * z.cap);
   z.prefix = take(sizeof(int64_t) * (z.cap + 1));
   z.first = take(sizeof(int32_t) * (batch + 1));
-  z.counters = take(sizeof(uint32_t) * G);
+  z.rec = take(sizeof(JoinRec) * G);
   z.part = take(sizeof(float) * split_part_floats<kPRows, kPD>() * 2 * G);
   z.total = at;
   return z;
@@ -1057,17 +1041,8 @@ cudaError_t launch_chunk(const PagedP& p, const PlanP& pl, const CUtensorMap& mk
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // The chunk kernel's set-up runs under the plan; it waits for the plan's end
   // before it reads anything.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.ctas);
-  cfg.blockDim = dim3(M::kThreads);
-  cfg.dynamicSmemBytes = M::kBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mk, mv, p, pl, box);
+  if ((e = launch_after(kern, dim3(pl.ctas), M::kThreads, M::kBytes, st, mk, mv, p, pl, box)) != cudaSuccess) return e;
+  return launch_after(chunk_join_kernel<kH>, dim3(pl.ctas, kPRows / kJoinRows), kJoinRows * 32, 0, st, p, pl);
 }
 
 }  // namespace
@@ -1101,7 +1076,7 @@ cudaError_t launch_paged_chunk(const PagedP& p, void* ws, cudaStream_t st) {
   pl.pair = reinterpret_cast<PlanPair*>(w + z.pair);
   pl.prefix = reinterpret_cast<int64_t*>(w + z.prefix);
   pl.first = reinterpret_cast<int32_t*>(w + z.first);
-  pl.counters = reinterpret_cast<uint32_t*>(w + z.counters);
+  pl.rec = reinterpret_cast<JoinRec*>(w + z.rec);
   pl.part = reinterpret_cast<float*>(w + z.part);
   pl.ctas = sm_count();
   pl.cap = z.cap;

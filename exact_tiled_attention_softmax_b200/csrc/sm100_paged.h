@@ -10,11 +10,10 @@ int sm_count();  // of the current device
 bool paged_pieces_ok(const PagedP& p);
 
 // Few new tokens a sequence: at most 16 rows (tokens x query heads of a
-// group) per K/V head. Bytes of workspace after the status block (counters
-// first, `zero` bytes of which must be cleared before the launch), and the
-// launch itself.
+// group) per K/V head. Bytes of workspace after the status block, and the
+// launch itself, which sets the status word (nothing needs clearing).
 bool paged_decode_supported(const PagedP& p, int32_t max_q);
-size_t paged_decode_workspace_bytes(size_t& zero);
+size_t paged_decode_workspace_bytes();
 cudaError_t launch_paged_decode(const PagedP& p, int32_t max_q, void* ws, cudaStream_t st);
 
 // Any number of new tokens: 256-row blocks on tcgen05. Its plan kernel clears
