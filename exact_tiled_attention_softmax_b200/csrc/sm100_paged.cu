@@ -9,14 +9,14 @@
 // place, O += P V into TMEM.
 //
 // K/V tiles of 128 keys come page by page: each lane of the producer warp
-// looks up the page of one box of the tile and issues its copies; boxes past
-// the sequence's end or in a page outside the pool are copied from past the
-// tensor's edge, that is as zeros. An e4m3 tile lands in a raw buffer, and four
+// looks up the page of one box of the tile and issues its copies (boxes past the
+// sequence's end or in a page outside the pool take page 0, whose keys are
+// masked). An e4m3 tile lands in a raw buffer, and four
 // warps turn it into the 16-bit operand tile (exact), while the row scales stay
 // fp32: K's multiplies the score, V's the probability.
 //
 // A masked key's V row may hold anything, and 0 times an infinity is not 0.
-// In tiles that some row sees only in part the checker warps (e4m3: the
+// In tiles that some row sees only in part, or that hold such a box, the checker warps (e4m3: the
 // converting ones) therefore take non-finite elements of V out of the operand;
 // rows that do see such a key get them back in the epilogue, where the result is
 // not finite whatever the probability was.
@@ -45,6 +45,7 @@ constexpr int kPD = 128;         // head width
 constexpr int kPTile = 128;      // keys per tile
 constexpr int kPRows = 256;      // query rows per block, two halves
 constexpr int kPStages = 2;      // K/V ring depth
+constexpr int kPlanSmem = 1024;  // blocks and sequences whose lists the plan keeps in shared memory
 constexpr int kPMinTiles = 2;    // tiles a CTA takes at least
 constexpr uint32_t kPTileB = kPTile * kPD * 2;  // 32 KB
 constexpr uint32_t kPRawB = kPTile * kPD;       // 16 KB, e4m3
@@ -63,8 +64,8 @@ struct PlanCta {
   int64_t u, left;          // its share: `left` tiles from tile index u on
   int32_t item, at, rank, pad;  // that is tile `at` of `item`; the share's number
 };
-struct PlanPair {
-  int32_t b, blk, tiles, pad;
+struct PlanPair {  // a block, with its sequence's view: one load names a piece
+  int32_t b, blk, tiles, q0, n, L, pad[2];
 };
 
 struct PlanP {
@@ -82,11 +83,11 @@ struct PlanP {
 };
 
 // Block blk of sequence b: its rows and the key tiles they see.
-__device__ __forceinline__ Item block_item(const PagedP& p, int tokens, int b, int blk) {
+__device__ __forceinline__ Item block_item(const PagedP& p, int tokens, const SeqView& s, int b, int blk) {
   Item it;
   it.b = b;
   it.h = 0;
-  it.s = seq_view(p.c, b);
+  it.s = s;
   const int group = p.Hq / p.c.Hkv;
   const int tok0 = blk * tokens, ntok = it.s.n - tok0 < tokens ? it.s.n - tok0 : tokens;
   it.row0 = tok0 * group;
@@ -124,7 +125,10 @@ __device__ __forceinline__ int last_at_most(const T* a, int n, T x) {
 
 __global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP pl) {
   __shared__ SplitShared ss;
-  __shared__ int64_t longest;
+  __shared__ int32_t longest[32];
+  // The lists are read many times over: from shared memory where they fit.
+  __shared__ int32_t s_first[kPlanSmem + 1], s_tiles[kPlanSmem];
+  __shared__ int64_t s_prefix[kPlanSmem + 1];
   dependents_may_launch();
   const CacheP& c = p.c;
   const int tid = threadIdx.x, n = blockDim.x, B = c.batch, Hkv = c.Hkv, G = pl.ctas;
@@ -132,33 +136,39 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP 
   for (int i = tid; i < G; i += n) pl.rec[i].parts = 0;
   __syncthreads();
   report_ragged(c);
+  int32_t* first = B <= kPlanSmem ? s_first : pl.first;
   int64_t before, carry = 0;
   for (int b0 = 0; b0 < B; b0 += n) {
     const int b = b0 + tid;
     const int64_t blocks = b < B ? (seq_view(c, b).n + pl.tokens - 1) / pl.tokens : 0;
     const int64_t sum = block_sum_scan(blocks, ss, before);
-    if (b < B) pl.first[b] = (int)(carry + before < pl.cap ? carry + before : pl.cap);
+    if (b < B) first[b] = (int)(carry + before < pl.cap ? carry + before : pl.cap);
     carry += sum;
   }
   // More blocks than cap only come from overlapping cu_q ranges (reported).
   const int NB = (int)(carry < pl.cap ? carry : pl.cap);
+  const bool small = NB <= kPlanSmem;
+  int64_t* prefix = small ? s_prefix : pl.prefix;
+  auto tiles_of = [&](int j) { return small ? s_tiles[j] : pl.pair[j].tiles; };
   __syncthreads();
   carry = 0;
   for (int j0 = 0; j0 < NB; j0 += n) {
     const int j = j0 + tid;
     int64_t units = 0;
     if (j < NB) {
-      const int i = NB - 1 - j, b = last_at_most(pl.first, B, i), blk = i - pl.first[b];
-      const int tiles = block_item(p, pl.tokens, b, blk).tiles;
-      pl.pair[j] = PlanPair{b, blk, tiles, 0};
+      const int i = NB - 1 - j, b = last_at_most(first, B, i), blk = i - first[b];
+      const SeqView sv = seq_view(c, b);
+      const int tiles = block_item(p, pl.tokens, sv, b, blk).tiles;
+      pl.pair[j] = PlanPair{b, blk, tiles, sv.q0, sv.n, (int)sv.L, {0, 0}};
+      if (small) s_tiles[j] = tiles;
       units = (int64_t)tiles * Hkv;
     }
     const int64_t sum = block_sum_scan(units, ss, before);
-    if (j < NB) pl.prefix[j] = carry + before;
+    if (j < NB) prefix[j] = carry + before;
     carry += sum;
   }
   const int64_t W = carry;
-  if (tid == 0) pl.prefix[NB] = W;
+  if (tid == 0) prefix[NB] = W;
   __syncthreads();
   const int NI = NB * Hkv;
   // Whole rounds, as many as leave no CTA (much) longer than the average.
@@ -167,21 +177,21 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP 
   int64_t whole = 0;
   const int most = rounds;
   for (int tries = 0; rounds > 0; ++tries) {
-    if (tid == 0) longest = 0;
-    __syncthreads();
     whole = 0;
     if (tid < G)
-      for (int r = 0; r < rounds; ++r) whole += pl.pair[(tid + r * G) / Hkv].tiles;
-    atomicMax(reinterpret_cast<unsigned long long*>(&longest), (unsigned long long)whole);
+      for (int r = 0; r < rounds; ++r) whole += tiles_of((tid + r * G) / Hkv);
+    const int top = __reduce_max_sync(0xffffffffu, (int)(whole < 0x7fffffff ? whole : 0x7fffffff));
     __syncthreads();
-    const bool fits = longest * 32 <= avg * 33;
+    if ((tid & 31) == 0) longest[tid >> 5] = top;
     __syncthreads();
+    const int64_t most_of = __reduce_max_sync(0xffffffffu, longest[tid & 31]);
+    const bool fits = most_of * 32 <= avg * 33;
     if (fits) break;
     rounds = tries == 0 ? rounds - 1 : tries == 1 ? most * 3 / 4 : tries == 2 ? most / 2 : 0;
   }
   if (rounds == 0) whole = 0;
   const int F = rounds * G;
-  const int64_t u0 = F < NI ? pl.prefix[F / Hkv] + (int64_t)(F % Hkv) * pl.pair[F / Hkv].tiles : W;
+  const int64_t u0 = F < NI ? prefix[F / Hkv] + (int64_t)(F % Hkv) * tiles_of(F / Hkv) : W;
   const int64_t rest = W - u0;
   int64_t active = (rest + kPMinTiles - 1) / kPMinTiles;
   active = active > G ? G : active;
@@ -195,8 +205,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP 
   if (tid < G) {
     PlanCta t{u, has ? end - u : 0, 0, 0, (int)rank, 0};
     if (has) {
-      const int j = last_at_most(pl.prefix, NB, u), tiles = pl.pair[j].tiles;
-      const int64_t rem = u - pl.prefix[j];
+      const int j = last_at_most(prefix, NB, u), tiles = tiles_of(j);
+      const int64_t rem = u - prefix[j];
       t.item = j * Hkv + (int)(rem / tiles);
       t.at = (int)(rem % tiles);
       pl.starts[rank] = u;
@@ -231,7 +241,7 @@ struct Pieces {
       return false;
     }
     const PlanPair pr = pl.pair[item / p.c.Hkv];
-    it = block_item(p, pl.tokens, pr.b, pr.blk);
+    it = block_item(p, pl.tokens, SeqView{pr.q0, pr.n, pr.L}, pr.b, pr.blk);
     it.h = item % p.c.Hkv;
     if (u < 0) {
       k0 = 0;
@@ -343,6 +353,96 @@ __device__ __forceinline__ void row_bits(const Halves& hv, int64_t pos, bool liv
     w0 &= ~range_bits64(i * box, i * box + box - 1);
     w1 &= ~range_bits64(i * box - 64, i * box + box - 65);
   }
+}
+
+// A masked row of a 16-bit tile, as softmax_masked_tile with its strict rules,
+// but 32-key groups that no row of the warp sees are skipped and groups that
+// all its rows see take no select: with a causal edge, rows of a warp (8
+// tokens of 4 heads, say) differ in few columns, and one group of the four
+// is mixed. 4.0 -> 1.9 us for a tile's two halves.
+template <bool kH>
+__device__ __forceinline__ float softmax_edge_tile(uint32_t tS, float scale_log2, uint64_t mw0, uint64_t mw1,
+                                                   float& m_run, float& l_run) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
+    if (!__any_sync(0xffffffffu, mw != 0u)) continue;
+    uint32_t r[32];
+    tmem_ld32(tS + q * 32, r);
+    tmem_wait_ld();
+    if (!__all_sync(0xffffffffu, mw == ~0u)) {
+      const float hide = scale_log2 >= 0.f ? -INFINITY : INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) r[e] = (mw >> e) & 1u ? r[e] : __float_as_uint(hide);
+    }
+    if (scale_log2 == 0.f) {  // 0 times the infinity that hides a key is not -inf
+      if (mw) mx = max3nan(mx, 0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (((mw >> e) & 1u) && !isfinite(__uint_as_float(r[e]))) mx = NAN;
+      continue;
+    }
+    float a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+    if (scale_log2 > 0.f) {
+#pragma unroll
+      for (int e = 2; e < 32; e += 2) {
+        a = max3nan(a, __uint_as_float(r[e]), a);
+        b = max3nan(b, __uint_as_float(r[e + 1]), b);
+      }
+      a = max3nan(a, b, b);
+    } else {
+#pragma unroll
+      for (int e = 2; e < 32; e += 2) {
+        a = min3nan(a, __uint_as_float(r[e]), a);
+        b = min3nan(b, __uint_as_float(r[e + 1]), b);
+      }
+      a = min3nan(a, b, b);
+    }
+    mx = max3nan(mx, a * scale_log2, mx);
+  }
+  const bool poison = !(mx < INFINITY);
+  if (poison) mx = -INFINITY;
+  const float alpha = move_max(mx, m_run);
+  const float msub = m_run == -INFINITY ? 0.f : m_run;
+  const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-msub, -msub);
+  uint64_t acc0 = 0ull, acc1 = 0ull;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
+    uint32_t pk[16];
+    if (!__any_sync(0xffffffffu, mw != 0u)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pk[e] = 0u;
+    } else {
+      uint32_t r[32];
+      tmem_ld32(tS + q * 32, r);
+      tmem_wait_ld();
+      const bool on = __all_sync(0xffffffffu, mw == ~0u);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), sc2, nm2), x0, x1);
+        x0 = ex2(x0);
+        x1 = ex2(x1);
+        if (!on) {
+          x0 = (mw >> (2 * e)) & 1u ? x0 : 0.f;
+          x1 = (mw >> (2 * e + 1)) & 1u ? x1 : 0.f;
+        }
+        if (e & 1)
+          acc1 = f2_add(acc1, f2_pack(x0, x1));
+        else
+          acc0 = f2_add(acc0, f2_pack(x0, x1));
+        pk[e] = pack16<kH>(x0, x1);
+      }
+    }
+    tmem_st16(tS + q * 16, pk);
+  }
+  float a0, a1, b0, b1;
+  f2_unpack(acc0, a0, a1);
+  f2_unpack(acc1, b0, b1);
+  l_run = poison ? NAN : l_run * alpha + ((a0 + a1) + (b0 + b1));
+  return alpha;
 }
 
 // The row of an e4m3 tile: scores times the keys' scales (which carry
@@ -467,6 +567,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   // TMEM columns: S/P of half w at 128 w, O of half w at 256 + 128 w.
+  // Q into L2 while the plan is made: every row is needed by some CTA soon.
+  // (The plan itself started after whatever wrote Q.)
+  {
+    const int64_t lines = (int64_t)c.rows * p.Hq * 2;  // 128-byte halves of rows
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < lines; i += (int64_t)gridDim.x * blockDim.x) {
+      const int64_t row = i >> 1, t = row / p.Hq;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + t * p.sq[0] + (row - t * p.Hq) * p.sq[1] + (i & 1) * 64;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+    }
+  }
   wait_for_previous();
   if constexpr (kQ8) {
     // 512 threads start with 128 registers each; the softmax warpgroups take
@@ -509,7 +619,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         const int s = n % kPStages;
         const uint32_t info = cls | (nk < k1 ? 16u : 0u) | __ballot_sync(0xffffffffu, pg == -1) << 8;
         const int off = (int)(((int64_t)it.tile_at(k) * kPTile + lane * box) % c.page_size);
-        const int page = pg < 0 ? c.num_pages : pg;
+        const int page = pg < 0 ? 0 : pg;  // whatever is there: masked, and made finite by the checkers
         if constexpr (!kQ8) {
           ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl->kv_empty[s]), ((n / kPStages) & 1) ^ 1, abort_flag, status));
           if (!ok) break;
@@ -674,12 +784,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         const int s = n % kPStages;
         const uint32_t par = (n / kPStages) & 1;
         const int64_t live = it.s.L - (int64_t)it.tile_at(k) * kPTile;  // rows of the tile inside the sequence
-        const bool part = in_part(cls);
+        bool part = in_part(cls);
         uint32_t ncls;
         const int nk = next_seen(it, hv, k + 1, k1, ncls);
         bool odd = false;
         if constexpr (!kQ8) {
           if (!(ok = wait_all(&ctl->v_full[s], par))) break;
+          part = part || ctl->tinfo[s] >> 8 != 0u;
           if (part) {
             const uint32_t expo = kHP ? 0x7c00u : 0x7f80u;
             const uint32_t base = kPV + s * kPTileB + ci * (kPTileB / 2);  // one 64-column half a warp
@@ -713,7 +824,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
           // K: wait for the raw tile and for the operand stage
           if (!(ok = wait_all(&ctl->raw_full[0], n & 1))) break;
           if (!(ok = wait_all(&ctl->kv_empty[s], par ^ 1))) break;
-          if (ci == 0 && lane == 0) ctl->tinfo[s] = ctl->raw_info;
+          const uint32_t info = ctl->raw_info;
+          if (ci == 0 && lane == 0) ctl->tinfo[s] = info;
+          part = part || info >> 8 != 0u;
           float* sc = reinterpret_cast<float*>(smem + M::kScale + s * 1024);
           sc[row] = ks;
           sc[128 + row] = vs;
@@ -796,23 +909,31 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     auto wait_all = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, wait_bar(smem_u32(bar), par, abort_flag, status));
     };
-    while (ok && pieces.next(p, pl, it, k0, k1, u)) {
+    bool have = pieces.next(p, pl, it, k0, k1, u);
+    while (ok && have) {
       hv.init(p, it);
       // ---- Q: a half-warp a row, 16 bytes a lane; rows past the block's are zero.
       // Every product of the previous piece has completed (o_final).
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int r = (warp & 3) * 32 + 2 * i + (lane >> 4), rr = 128 * w + r;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < it.rows) {
-          int64_t tok;
-          int h;
-          row_place(p, it, rr, tok, h);
-          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + tok * p.sq[0] + h * p.sq[1] +
-                                              (lane & 15) * 8);
+      {
+        uint4 v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int rr = 128 * w + (warp & 3) * 32 + 2 * i + (lane >> 4);
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < it.rows) {
+            int64_t tok;
+            int h;
+            row_place(p, it, rr, tok, h);
+            v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + tok * p.sq[0] + h * p.sq[1] +
+                                                   (lane & 15) * 8);
+          }
         }
-        const uint32_t dst = kPQ + w * kPTileB + ((lane >> 3) & 1) * (kPTileB / 2) + sw128_offset(r, (lane & 7) * 16);
-        *reinterpret_cast<uint4*>(smem + dst) = v;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = (warp & 3) * 32 + 2 * i + (lane >> 4);
+          const uint32_t dst = kPQ + w * kPTileB + ((lane >> 3) & 1) * (kPTileB / 2) + sw128_offset(r, (lane & 7) * 16);
+          *reinterpret_cast<uint4*>(smem + dst) = v[i];
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -838,7 +959,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         if constexpr (!kQ8) {
           const float sl2 = p.scale * kLog2e;
           alpha = full ? softmax_full_tile<kH, false, true>(tS, sl2, m_run, l_run, ~0ull, ~0ull)
-                       : softmax_masked_tile<kH, true>(tS, sl2, w0, w1, ~0ull, ~0ull, m_run, l_run);
+                       : softmax_edge_tile<kH>(tS, sl2, w0, w1, m_run, l_run);
         } else {
           const float* sc = reinterpret_cast<const float*>(smem + M::kScale + s * 1024);
           alpha = full ? softmax_scaled_tile<false>(tS, sc, sc + 128, w0, w1, m_run, l_run)
@@ -862,7 +983,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         ++got;
         ++mine;
       }
-      if (!ok || !(ok = wait_all(&ctl->o_final, piece & 1))) break;
+      if (!ok) break;
+      // The next piece, and its rows' Q into L2, while the last products run.
+      Item nit;
+      int nk0 = 0, nk1 = 0;
+      int64_t nu = 0;
+      have = pieces.next(p, pl, nit, nk0, nk1, nu);
+      if (have && 128 * w + t < nit.rows) {
+        int64_t tok;
+        int h;
+        row_place(p, nit, 128 * w + t, tok, h);
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + tok * p.sq[0] + h * p.sq[1];
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+      }
+      if (!(ok = wait_all(&ctl->o_final, piece & 1))) break;
       tc_fence_after();
       // ---- epilogue: the rows, or this piece's part of them
       const bool whole = k0 == 0 && k1 == it.tiles;
@@ -888,7 +1023,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
           uint32_t c2;
 #pragma unroll 1
           for (int k = next_seen(it, hv, k0, k1, c2); k < k1; k = next_seen(it, hv, k + 1, k1, c2)) {
-            if (!in_part(c2)) continue;
             const int kt = it.tile_at(k);
             uint64_t w0, w1;
             row_bits(hv, pos, valid, kt, 0u, box, w0, w1);
@@ -920,8 +1054,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         } else if (valid) {
 #pragma unroll
           for (int c4 = 0; c4 < 8; ++c4)
-            __stcg(reinterpret_cast<uint4*>(slot + (size_t)rr * kPD + ch * 32) + c4,
-                   make_uint4(o[4 * c4], o[4 * c4 + 1], o[4 * c4 + 2], o[4 * c4 + 3]));
+            reinterpret_cast<uint4*>(slot)[(ch * 8 + c4) * kPRows + rr] =
+                make_uint4(o[4 * c4], o[4 * c4 + 1], o[4 * c4 + 2], o[4 * c4 + 3]);
         }
       }
       if (valid && whole) p.lse[tok * p.sl[0] + h * p.sl[1]] = lse;
@@ -932,12 +1066,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         }
         if (k0 == 0 && w == 0 && t == 0) {
           const int last = last_at_most(pl.starts, pieces.head.ranks, u + it.tiles - 1);
-          JoinRec rec{last - pieces.mine.rank + 1, it.s.q0, it.row0, it.rows, it.h, 0u, {0, 0}};
+          const JoinRec rec{last - pieces.mine.rank + 1, it.s.q0, it.row0, it.rows, it.h, 0u, {0, 0}};
           pl.rec[pieces.mine.rank] = rec;
         }
       }
       tc_fence_before();
       ++piece;
+      it = nit;
+      k0 = nk0;
+      k1 = nk1;
+      u = nu;
     }
   }
   tc_fence_before();
@@ -948,12 +1086,71 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
   }
 }
 
+// The joins that the records ask for. A piece's rows lie four columns at a time
+// ([32][256 rows] float4), as the row-per-thread epilogue writes them in whole
+// lines; a warp joins 8 rows x 32 columns (lane: row lane % 8, columns
+// 4 (lane / 8) and so on), and block (share, y) the rows 32 y .. of its record.
+constexpr int kJoinBlockRows = 32;
+
 template <bool kH>
-__global__ void __launch_bounds__(kJoinRows * 32) chunk_join_kernel(const PagedP p, const PlanP pl) {
+__global__ void __launch_bounds__(512) chunk_join_kernel(const PagedP p, const PlanP pl) {
   wait_for_previous();
-  join_record<kPRows, kPD, kH>(p, pl.rec, pl.ctas, false, [&](int i, int e) {
-    return split_slot<kPRows, kPD>(SplitP{0, 0, nullptr, pl.part}, pl.cta_of[i + e], e == 0 ? 1 : 0);
-  });
+  const JoinRec rec = pl.rec[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.y * kJoinBlockRows + (warp >> 2) * 8 + (lane & 7);
+  if (rec.parts == 0 || r - (lane & 7) >= rec.rows) return;
+  const bool live = r < rec.rows;
+  const int c4 = (warp & 3) * 8 + (lane >> 3);  // and c4 + 4
+  auto at = [&](int i) {
+    return split_slot<kPRows, kPD>(SplitP{0, 0, nullptr, pl.part}, pl.cta_of[blockIdx.x + i], i == 0 ? 1 : 0);
+  };
+  float M = -INFINITY, L = 0.f;
+  float4 v[2];
+  v[0] = v[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // A running maximum over the pieces, four of them in flight.
+  for (int i0 = 0; i0 < rec.parts; i0 += 4) {
+    float m[4], l[4];
+    float4 x[4][2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      m[e] = -INFINITY;
+      l[e] = 0.f;
+      x[e][0] = x[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + e < rec.parts && live) {
+        const float* s = at(i0 + e);
+        m[e] = s[kPRows * kPD + r];
+        l[e] = s[kPRows * kPD + kPRows + r];
+        x[e][0] = reinterpret_cast<const float4*>(s)[c4 * kPRows + r];
+        x[e][1] = reinterpret_cast<const float4*>(s)[(c4 + 4) * kPRows + r];
+      }
+    }
+    const float top = fmaxf(fmaxf(fmaxf(M, m[0]), fmaxf(m[1], m[2])), m[3]);
+    const float old = part_factor(M, top);
+    L *= old;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) v[a] = make_float4(v[a].x * old, v[a].y * old, v[a].z * old, v[a].w * old);
+    M = top;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i0 + e >= rec.parts) break;
+      const float f = part_factor(m[e], M);
+      L += l[e] * f;
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        v[a].x = fmaf(x[e][a].x, f, v[a].x);
+        v[a].y = fmaf(x[e][a].y, f, v[a].y);
+        v[a].z = fmaf(x[e][a].z, f, v[a].z);
+        v[a].w = fmaf(x[e][a].w, f, v[a].w);
+      }
+    }
+  }
+  if (!live) return;
+  Item it;
+  it.s.q0 = rec.q0;
+  it.row0 = rec.row0;
+  it.h = rec.h;
+  finish_four<kH>(p, it, r, c4, M, L, v[0]);
+  finish_four<kH>(p, it, r, c4 + 4, M, L, v[1]);
 }
 
 // ----------------------------------------------------------- host helpers
@@ -1042,7 +1239,7 @@ cudaError_t launch_chunk(const PagedP& p, const PlanP& pl, const CUtensorMap& mk
   // The chunk kernel's set-up runs under the plan; it waits for the plan's end
   // before it reads anything.
   if ((e = launch_after(kern, dim3(pl.ctas), M::kThreads, M::kBytes, st, mk, mv, p, pl, box)) != cudaSuccess) return e;
-  return launch_after(chunk_join_kernel<kH>, dim3(pl.ctas, kPRows / kJoinRows), kJoinRows * 32, 0, st, p, pl);
+  return launch_after(chunk_join_kernel<kH>, dim3(pl.ctas, kPRows / kJoinBlockRows), 512, 0, st, p, pl);
 }
 
 }  // namespace

@@ -142,11 +142,10 @@ __device__ __forceinline__ float softmax_full_tile(uint32_t tS, float scale_log2
 // columns per pass for the exponentials. The sum and the maximum use
 // every allowed key (undropped); P carries only the kept ones (the 1/(1-rho)
 // factor is applied to O in fp32 at the end). Returns alpha.
-template <bool kH, bool kStrict = false>
+template <bool kH>
 __device__ __forceinline__ float softmax_masked_tile(uint32_t tS, float scale_log2, uint64_t mw0, uint64_t mw1,
                                                      uint64_t kb0, uint64_t kb1, float& m_run, float& l_run) {
   float mx = -INFINITY;
-  bool poison = false;
 #pragma unroll 1
   for (int hf = 0; hf < 2; ++hf) {
     uint32_t r0[32], r1[32];
@@ -156,14 +155,10 @@ __device__ __forceinline__ float softmax_masked_tile(uint32_t tS, float scale_lo
     const uint64_t mw = hf ? mw1 : mw0;
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-      const float x0 = __uint_as_float(r0[e]) * scale_log2, x1 = __uint_as_float(r1[e]) * scale_log2;
-      if ((mw >> e) & 1ull) mx = fmaxf(mx, x0);
-      if ((mw >> (32 + e)) & 1ull) mx = fmaxf(mx, x1);
-      if constexpr (kStrict)
-        poison = poison || (((mw >> e) & 1ull) && !(x0 < INFINITY)) || (((mw >> (32 + e)) & 1ull) && !(x1 < INFINITY));
+      if ((mw >> e) & 1ull) mx = fmaxf(mx, __uint_as_float(r0[e]) * scale_log2);
+      if ((mw >> (32 + e)) & 1ull) mx = fmaxf(mx, __uint_as_float(r1[e]) * scale_log2);
     }
   }
-  if (poison) mx = -INFINITY;
   const float alpha = move_max(mx, m_run);
   const float msub = m_run == -INFINITY ? 0.f : m_run;
   float sum = 0.f;
@@ -186,7 +181,7 @@ __device__ __forceinline__ float softmax_masked_tile(uint32_t tS, float scale_lo
     }
     tmem_st16(tS + q * 16, pk);
   }
-  l_run = poison ? NAN : l_run * alpha + sum;
+  l_run = l_run * alpha + sum;
   return alpha;
 }
 
