@@ -123,9 +123,11 @@ __device__ __forceinline__ int last_at_most(const T* a, int n, T x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP pl) {
+constexpr int kPlanThreads = 256;  // at least one per CTA
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PagedP p, const PlanP pl) {
   __shared__ SplitShared ss;
-  __shared__ int32_t longest[32];
+  __shared__ int32_t longest[kPlanThreads / 32];
   // The lists are read many times over: from shared memory where they fit.
   __shared__ int32_t s_first[kPlanSmem + 1], s_tiles[kPlanSmem];
   __shared__ int64_t s_prefix[kPlanSmem + 1];
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PagedP p, const PlanP 
     __syncthreads();
     if ((tid & 31) == 0) longest[tid >> 5] = top;
     __syncthreads();
-    const int64_t most_of = __reduce_max_sync(0xffffffffu, longest[tid & 31]);
+    const int64_t most_of = __reduce_max_sync(0xffffffffu, longest[tid & (kPlanThreads / 32 - 1)]);
     const bool fits = most_of * 32 <= avg * 33;
     if (fits) break;
     rounds = tries == 0 ? rounds - 1 : tries == 1 ? most * 3 / 4 : tries == 2 ? most / 2 : 0;
@@ -529,8 +531,9 @@ struct Tag {
 
 template <bool kH, bool kQ8>
 __global__ void __launch_bounds__(PagedSmem<kQ8>::kThreads, 1)
-paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                   const __grid_constant__ PagedP p, const __grid_constant__ PlanP pl, int box) {
+paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedP p,
+                   const __grid_constant__ PlanP pl, int box, int q_boxes) {
   using M = PagedSmem<kQ8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -542,7 +545,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
   constexpr bool kHP = kH && !kQ8;  // P and V in fp16, else bf16
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&ctl->q_full), 8);
+    mbar_init(smem_u32(&ctl->q_full), q_boxes ? 1 : 8);
     for (int s = 0; s < kPStages; ++s) {
       mbar_init(smem_u32(&ctl->raw_full[s]), 1);
       mbar_init(smem_u32(&ctl->raw_empty[s]), M::kCheckers);
@@ -567,16 +570,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   // TMEM columns: S/P of half w at 128 w, O of half w at 256 + 128 w.
-  // Q into L2 while the plan is made: every row is needed by some CTA soon.
-  // (The plan itself started after whatever wrote Q.)
-  {
-    const int64_t lines = (int64_t)c.rows * p.Hq * 2;  // 128-byte halves of rows
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < lines; i += (int64_t)gridDim.x * blockDim.x) {
-      const int64_t row = i >> 1, t = row / p.Hq;
-      const uint16_t* q = static_cast<const uint16_t*>(p.q) + t * p.sq[0] + (row - t * p.Hq) * p.sq[1] + (i & 1) * 64;
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-    }
-  }
   wait_for_previous();
   if constexpr (kQ8) {
     // 512 threads start with 128 registers each; the softmax warpgroups take
@@ -661,7 +654,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         pg = npg;
       }
     }
-    // Every copy lands before the CTA's shared memory goes.
+    // Every copy lands before the CTA's shared memory goes. (Q's are waited for by
+    // the warp that issues them.)
     if constexpr (!kQ8) {
       for (int r = (n > kPStages ? n - kPStages : 0); r < n; ++r) {
         wait_bar(smem_u32(&ctl->k_full[r % kPStages]), (r / kPStages) & 1, abort_flag, nullptr);
@@ -700,6 +694,25 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
       hv.init(p, it);
       uint32_t cls;
       const bool any = next_seen(it, hv, k0, k1, cls) < k1;
+      if (q_boxes) {
+        // Q, once the previous piece's products have read the last one: two
+        // boxes of (64 columns, the group's heads, 128 / group tokens) a half.
+        // Rows past the block's belong to other tokens; their results go
+        // nowhere. The softmax warps may still be writing the previous piece:
+        // its O and this piece's S are different columns.
+        if (piece > 0 && !(ok = wait_all(&ctl->o_final, (piece - 1) & 1))) break;
+        if (leader) {
+          const uint32_t qf = smem_u32(&ctl->q_full);
+          const int group = p.Hq / c.Hkv, halves = it.rows > 128 ? 2 : 1;
+          mbar_expect_tx(qf, halves * kPTileB);
+          for (int w = 0; w < halves; ++w) {
+            const int tok = it.s.q0 + it.row0 / group + w * (128 / group);
+            tma_load_3d(sbase + kPQ + w * kPTileB, &tq, qf, 0, it.h * group, tok);
+            tma_load_3d(sbase + kPQ + w * kPTileB + kPTileB / 2, &tq, qf, 64, it.h * group, tok);
+          }
+        }
+        __syncwarp();
+      }
       if (!(ok = wait_all(&ctl->q_full, piece & 1))) break;
       tc_fence_after();
       uint32_t info = 0;
@@ -912,9 +925,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     bool have = pieces.next(p, pl, it, k0, k1, u);
     while (ok && have) {
       hv.init(p, it);
-      // ---- Q: a half-warp a row, 16 bytes a lane; rows past the block's are zero.
-      // Every product of the previous piece has completed (o_final).
-      {
+      // ---- Q, where the heads of a group do not divide a half into whole tokens:
+      // a half-warp a row, 16 bytes a lane; rows past the block's are zero. Every
+      // product of the previous piece has completed (o_final).
+      if (!q_boxes) {
         uint4 v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -934,10 +948,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
           const uint32_t dst = kPQ + w * kPTileB + ((lane >> 3) & 1) * (kPTileB / 2) + sw128_offset(r, (lane & 7) * 16);
           *reinterpret_cast<uint4*>(smem + dst) = v[i];
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full));
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full));
 
       const int rr = 128 * w + t;
       const bool valid = rr < it.rows;
@@ -989,7 +1003,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
       int nk0 = 0, nk1 = 0;
       int64_t nu = 0;
       have = pieces.next(p, pl, nit, nk0, nk1, nu);
-      if (have && 128 * w + t < nit.rows) {
+      if (!q_boxes && have && 128 * w + t < nit.rows) {
         int64_t tok;
         int h;
         row_place(p, nit, 128 * w + t, tok, h);
@@ -1185,6 +1199,19 @@ bool pool_map(CUtensorMap* map, const void* base, const CacheP& c, const int64_t
          CUDA_SUCCESS;
 }
 
+// 3-D map of Q over (d, head, token) with a (64, group, 128 / group) box.
+bool q_map(CUtensorMap* map, const PagedP& p, int group) {
+  auto fn = paged_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kPD, (cuuint64_t)p.Hq, (cuuint64_t)p.c.rows};
+  cuuint64_t strides[2] = {(cuuint64_t)p.sq[1] * 2, (cuuint64_t)p.sq[0] * 2};
+  cuuint32_t bx[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(map, p.dtype == ATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(p.q), dims, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Keys per copy box: the largest power of two up to 128 that divides the page.
 int box_of(int page_size) {
   int b = 16;
@@ -1221,8 +1248,8 @@ PlanSizes plan_sizes(int64_t rows, int batch, int group) {
 }
 
 template <bool kH, bool kQ8>
-cudaError_t launch_chunk(const PagedP& p, const PlanP& pl, const CUtensorMap& mk, const CUtensorMap& mv, int box,
-                         cudaStream_t st) {
+cudaError_t launch_chunk(const PagedP& p, const PlanP& pl, const CUtensorMap& mq, const CUtensorMap& mk,
+                         const CUtensorMap& mv, int box, int q_boxes, cudaStream_t st) {
   using M = PagedSmem<kQ8>;
   auto kern = paged_chunk_kernel<kH, kQ8>;
   static bool done[64] = {};
@@ -1234,18 +1261,19 @@ cudaError_t launch_chunk(const PagedP& p, const PlanP& pl, const CUtensorMap& mk
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = true;
   }
-  plan_kernel<<<1, 1024, 0, st>>>(p, pl);
+  plan_kernel<<<1, kPlanThreads, 0, st>>>(p, pl);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // The chunk kernel's set-up runs under the plan; it waits for the plan's end
   // before it reads anything.
-  if ((e = launch_after(kern, dim3(pl.ctas), M::kThreads, M::kBytes, st, mk, mv, p, pl, box)) != cudaSuccess) return e;
+  if ((e = launch_after(kern, dim3(pl.ctas), M::kThreads, M::kBytes, st, mq, mk, mv, p, pl, box,
+                        q_boxes)) != cudaSuccess) return e;
   return launch_after(chunk_join_kernel<kH>, dim3(pl.ctas, kPRows / kJoinBlockRows), 512, 0, st, p, pl);
 }
 
 }  // namespace
 
 bool paged_chunk_supported(const PagedP& p) {
-  if (!paged_pieces_ok(p) || p.Hq / p.c.Hkv > kPRows || sm_count() > 1024 || !paged_encode_fn()) return false;
+  if (!paged_pieces_ok(p) || p.Hq / p.c.Hkv > kPRows || sm_count() > kPlanThreads || !paged_encode_fn()) return false;
   const CacheP& c = p.c;
   // What a tensor map can describe: positive strides below 2^40 bytes.
   for (int i = 0; i < 3; ++i)
@@ -1279,12 +1307,18 @@ cudaError_t launch_paged_chunk(const PagedP& p, void* ws, cudaStream_t st) {
   pl.cap = z.cap;
   pl.tokens = kPRows / (p.Hq / c.Hkv);
   const int box = box_of(c.page_size);
-  CUtensorMap mk, mv;
+  // A copy box holds whole tokens of a group where the group divides a half.
+  const int group = p.Hq / c.Hkv;
+  const int q_boxes = 128 % group == 0 && p.sq[0] > 0 && p.sq[1] > 0 && p.sq[0] < (1LL << 38) && p.sq[1] < (1LL << 38);
+  CUtensorMap mq = {}, mk, mv;
+  if (q_boxes && !q_map(&mq, p, group)) return cudaErrorInvalidValue;
   if (!pool_map(&mk, c.k, c, c.sk, box) || !pool_map(&mv, c.v, c, c.sv, box)) return cudaErrorInvalidValue;
   const bool h = p.dtype == ATTN_F16;
   if (c.dtype == ATTN_E4M3)
-    return h ? launch_chunk<true, true>(p, pl, mk, mv, box, st) : launch_chunk<false, true>(p, pl, mk, mv, box, st);
-  return h ? launch_chunk<true, false>(p, pl, mk, mv, box, st) : launch_chunk<false, false>(p, pl, mk, mv, box, st);
+    return h ? launch_chunk<true, true>(p, pl, mq, mk, mv, box, q_boxes, st)
+             : launch_chunk<false, true>(p, pl, mq, mk, mv, box, q_boxes, st);
+  return h ? launch_chunk<true, false>(p, pl, mq, mk, mv, box, q_boxes, st)
+           : launch_chunk<false, false>(p, pl, mq, mk, mv, box, q_boxes, st);
 }
 
 }  // namespace attn
