@@ -187,12 +187,15 @@ def _check_on(device: torch.device, *tensors) -> None:
             raise ValueError(f"a tensor is on {t.device}, the query on {device}")
 
 
+_INT32, _ONE_DIM, _TWO_DIMS = (torch.int32,), (1,), (2,)
+
+
 def _check_mask_tensor(t: torch.Tensor, name: str, dtypes, dims) -> None:
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
     if t.dim() not in dims:
         raise ValueError(f"{name}: {t.dim()} dimensions, expected {' or '.join(map(str, dims))}")
-    if t.numel() > 1 and t.stride(-1) != 1:
+    if not t.is_contiguous() and t.numel() > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the innermost dimension must be contiguous")
 
 
@@ -486,8 +489,8 @@ class PagedCache:
     def to_c(self) -> AttnCacheC:
         """The C descriptor, after the checks that raw pointers cannot carry."""
         table, lens = self.block_table, self.seq_lens
-        _check_mask_tensor(table, "block_table", (torch.int32,), (2,))
-        _check_mask_tensor(lens, "seq_lens", (torch.int32,), (1,))
+        _check_mask_tensor(table, "block_table", _INT32, _TWO_DIMS)
+        _check_mask_tensor(lens, "seq_lens", _INT32, _ONE_DIM)
         B, pages = table.shape
         if B != lens.shape[0]:
             raise ValueError("block_table and seq_lens hold different numbers of sequences")
@@ -502,20 +505,21 @@ class PagedCache:
 def _cu_q_ptr(cu_q, cache: PagedCache):
     if cu_q is None:
         return None
-    _check_mask_tensor(cu_q, "cu_q", (torch.int32,), (1,))
+    _check_mask_tensor(cu_q, "cu_q", _INT32, _ONE_DIM)
     if cu_q.shape[0] != cache.seq_lens.shape[0] + 1:
         raise ValueError(f"cu_q holds {cu_q.shape[0]} entries, expected one more than the sequences")
     _check_on(cache.k.device, cu_q)
     return cu_q.data_ptr()
 
 
-def _launch_on(device: torch.device, call, stream) -> int:
-    """call(stream handle) with `device` current: the library launches on the
-    current device, and the default stream is that device's current one."""
+def _on_device(device: torch.device, call, stream, *args) -> int:
+    """call(*args, stream handle) with `device` current: the library launches
+    on the current device, and the default stream is that device's current
+    one."""
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return call(_stream_handle(stream))
-    return call(_stream_handle(stream))
+            return call(*args, _stream_handle(stream))
+    return call(*args, _stream_handle(stream))
 
 
 def _workspace_args(workspace) -> tuple:
@@ -527,11 +531,11 @@ def attn_cache_write(k, v, cache: PagedCache, cu_q=None, *, workspace=None, stre
     of the cache's sequences (cu_q int32 [batch + 1]; None: the same number
     each), quantised when the cache is e4m3. With a workspace of at least 256
     bytes, attn_get_status reports bad pages and lengths. Returns the cache."""
-    ck, cv, c = _tensor(k), _tensor(v), cache.to_c()
-    cu = _cu_q_ptr(cu_q, cache)
-    _check_on(cache.k.device, k, v, workspace)
-    rc = _launch_on(k.device, lambda s: load_library().attn_cache_write(
-        _ref(ck), _ref(cv), cu, _ref(c), *_workspace_args(workspace), s), stream)
+    device = cache.k.device
+    c, cu = cache.to_c(), _cu_q_ptr(cu_q, cache)
+    _check_on(device, k, v, workspace)
+    rc = _on_device(device, load_library().attn_cache_write, stream, _tensor(k), _tensor(v), cu, c,
+                    *_workspace_args(workspace))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_write")
     return cache
@@ -544,28 +548,28 @@ def attn_cache_read(cache: PagedCache, max_len: int | None = None, *, dtype=None
     sequence's length are left as they were in k and v given by the caller and
     are zero in new ones. dtype (new tensors): default the pool's, bfloat16
     for an e4m3 pool."""
+    device = cache.k.device
     if k is None or v is None:
-        P, page, H, d = cache.k.shape
+        _, page, H, d = cache.k.shape
         T = int(max_len) if max_len is not None else cache.block_table.shape[1] * page
         if dtype is None:
             dtype = torch.bfloat16 if cache.k.dtype == torch.float8_e4m3fn else cache.k.dtype
         B = cache.seq_lens.shape[0]
-        k = torch.zeros(B, H, T, d, dtype=dtype, device=cache.k.device) if k is None else k
-        v = torch.zeros(B, H, T, cache.v.shape[3], dtype=dtype, device=cache.k.device) if v is None else v
-    ck, cv, c = _tensor(k), _tensor(v), cache.to_c()
-    _check_on(cache.k.device, k, v, workspace)
-    rc = _launch_on(k.device, lambda s: load_library().attn_cache_read(
-        _ref(c), _ref(ck), _ref(cv), *_workspace_args(workspace), s), stream)
+        k = torch.zeros(B, H, T, d, dtype=dtype, device=device) if k is None else k
+        v = torch.zeros(B, H, T, cache.v.shape[3], dtype=dtype, device=device) if v is None else v
+    c = cache.to_c()
+    _check_on(device, k, v, workspace)
+    rc = _on_device(device, load_library().attn_cache_read, stream, c, _tensor(k), _tensor(v),
+                    *_workspace_args(workspace))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_read")
     return k, v
 
 
 def attn_paged_workspace_size(q, cache: PagedCache, allowed: AllowedSet | None = None) -> int:
-    cq, c = _tensor(q), cache.to_c()
     m = allowed.to_c() if allowed else None
     with torch.cuda.device(q.device):
-        return int(load_library().attn_paged_workspace_size(_ref(cq), _ref(c), _ref(m)))
+        return int(load_library().attn_paged_workspace_size(_tensor(q), cache.to_c(), m))
 
 
 def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None = None, scale: float | None = None, *,
@@ -576,31 +580,30 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
     LSE formats. max_q: the largest number of new tokens of a sequence, when
     known (it only chooses between kernels). Returns (o [rows, Hq, dv], lse
     [rows, Hq])."""
-    lib = load_library()
+    lib, device = load_library(), q.device
+    rows, heads, d = q.shape
     if scale is None:
-        scale = q.shape[-1] ** -0.5
+        scale = d ** -0.5
     if out is None:
-        out = torch.empty(*q.shape[:-1], cache.v.shape[-1], dtype=q.dtype, device=q.device)
+        out = torch.empty((rows, heads, cache.v.shape[3]), dtype=q.dtype, device=device)
     if lse is None:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
     m = allowed.to_c() if allowed else None
-    cq, co, cl, c = _tensor(q), _tensor(out), _tensor(lse), cache.to_c()
-    cu = _cu_q_ptr(cu_q, cache)
-    _check_on(cache.k.device, q, out, lse, workspace, *(allowed.tensors() if allowed else ()))
+    cq, c, cu = _tensor(q), cache.to_c(), _cu_q_ptr(cu_q, cache)
+    _check_on(device, cache.k, out, lse, workspace, *(allowed.tensors() if allowed else ()))
 
     def call(s):
         ws = workspace
         if ws is None:
-            need = lib.attn_paged_workspace_size(_ref(cq), _ref(c), _ref(m))
+            need = lib.attn_paged_workspace_size(cq, c, m)
             if stream is None:
-                ws = _workspace(need, q.device)
+                ws = _workspace(need, device)
             else:  # from that stream's pool: freed here, reused there after the call
                 with torch.cuda.stream(stream):
-                    ws = _workspace(need, q.device)
-        return lib.attn_paged_fwd(_ref(cq), cu, _ref(c), _ref(m), ctypes.c_float(scale), int(max_q), _ref(co),
-                                  _ref(cl), *_workspace_args(ws), s)
+                    ws = _workspace(need, device)
+        return lib.attn_paged_fwd(cq, cu, c, m, scale, int(max_q), _tensor(out), _tensor(lse), *_workspace_args(ws), s)
 
-    rc = _launch_on(q.device, call, stream)
+    rc = _on_device(device, call, stream)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_paged_fwd")
     return out, lse

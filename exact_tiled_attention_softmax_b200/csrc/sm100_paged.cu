@@ -262,13 +262,15 @@ struct Pieces {
 
 // What the two halves of a block see of a tile.
 struct Halves {
+  // Positions, lengths and windows are below 2^30 (the cache's limit), so that
+  // their sums and differences fit 32 bits.
   int rows[2];
-  int64_t p0[2], p1[2];  // positions of the half's first and last token
-  int64_t L, window, first;
+  int p0[2], p1[2];  // positions of the half's first and last token
+  int L, window, first;
   bool causal, win;
   __device__ __forceinline__ void init(const PagedP& p, const Item& it) {
     const int group = p.Hq / p.c.Hkv;
-    const int64_t base = it.s.L - it.s.n;
+    const int base = (int)it.s.L - it.s.n;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       rows[w] = it.rows - 128 * w;
@@ -276,15 +278,15 @@ struct Halves {
       p0[w] = base + (it.row0 + 128 * w) / group;
       p1[w] = base + (it.row0 + 128 * w + rows[w] - 1) / group;
     }
-    L = it.s.L;
+    L = (int)it.s.L;
     causal = p.flags & ATTN_MASK_CAUSAL;
     win = p.flags & ATTN_MASK_WINDOW;
-    window = p.window;
-    first = p.first;
+    window = (int)p.window;
+    first = (int)p.first;
   }
   // kEmptyH: no row of half w sees a key of tile kt; kFullH: all see all.
   __device__ __forceinline__ int cls(int w, int kt) const {
-    const int64_t c0 = (int64_t)kt * kPTile, c1 = c0 + kPTile - 1;
+    const int c0 = kt * kPTile, c1 = c0 + kPTile - 1;
     if (rows[w] == 0 || c0 >= L || p1[w] < 0) return 0;
     if (causal && c0 > p1[w]) return 0;
     if (win && c0 >= first && c1 <= p0[w] - window) return 0;
@@ -316,6 +318,7 @@ struct PagedCtl {
   uint32_t tmem_base;
   uint32_t abort_flag;
   uint32_t odd_piece;  // 1 + the piece whose V tiles lost non-finite elements
+  float ks_top[kPStages][4], ks_low[kPStages][4];  // e4m3: the K scales' extremes, by 32 keys
   // Per stage: bits 0-3 the halves' classes, bit 4 another tile follows, bits
   // 8-15 boxes in pages outside the pool. raw_info: the same, with the raw K tile.
   uint32_t tinfo[kPStages];
@@ -324,7 +327,7 @@ struct PagedCtl {
 
 template <bool kQ8>
 struct PagedSmem {
-  static constexpr uint32_t kScale = kPRaw + (kQ8 ? 2 * kPRawB : 0);  // kPStages x (128 K, 128 V) fp32
+  static constexpr uint32_t kScale = kPRaw + (kQ8 ? 2 * kPRawB : 0);  // kPStages x (128 K, 128 V scales) fp32
   static constexpr uint32_t kCtl = kScale + (kQ8 ? kPStages * 1024 : 0);
   static constexpr uint32_t kBytes = kCtl + 512;
   static constexpr int kThreads = kQ8 ? 512 : 384;
@@ -333,19 +336,19 @@ struct PagedSmem {
 static_assert(sizeof(PagedCtl) <= 512, "control block");
 
 // Row i's keys of tile kt as two 64-bit words.
-__device__ __forceinline__ void row_bits(const Halves& hv, int64_t pos, bool live, int kt, uint32_t bad, int box,
+__device__ __forceinline__ void row_bits(const Halves& hv, int pos, bool live, int kt, uint32_t bad, int box,
                                          uint64_t& w0, uint64_t& w1) {
-  const int64_t j0 = (int64_t)kt * kPTile;
+  const int j0 = kt * kPTile;
   w0 = w1 = 0ull;
   if (!live || pos < 0) return;
-  int64_t hi = hv.L - 1;
+  int hi = hv.L - 1;
   if (hv.causal && pos < hi) hi = pos;
-  int64_t lo = j0;
+  int lo = j0;
   if (hv.win && pos - hv.window + 1 > lo) lo = pos - hv.window + 1;
   w0 = range_bits64(lo - j0, hi - j0);
   w1 = range_bits64(lo - j0 - 64, hi - j0 - 64);
   if (hv.win && j0 < hv.first) {
-    const int64_t fh = hv.first - 1 < hi ? hv.first - 1 : hi;
+    const int fh = hv.first - 1 < hi ? hv.first - 1 : hi;
     w0 |= range_bits64(0, fh - j0);
     w1 |= range_bits64(-64, fh - j0 - 64);
   }
@@ -448,34 +451,67 @@ __device__ __forceinline__ float softmax_edge_tile(uint32_t tS, float scale_log2
 }
 
 // The row of an e4m3 tile: scores times the keys' scales (which carry
-// c log2(e)), probabilities times the V rows' scales before they are rounded.
-// Like the 16-bit rows' functions otherwise, with their strict rules.
+// c log2(e)), probabilities times the V rows' scales before they are rounded
+// to bf16. The running summary needs no exact maximum, only a reference m
+// that keeps 2^(x - m) inside fp32's range and never above 2^8 of it: where the
+// tile's K scales lie within a factor of 4 (top, low) and no score passes 100
+// in base 2, the largest unscaled score times `top` (`low`, if it is negative)
+// is above every scaled one by less than 100, and the probabilities keep their
+// relative precision in fp32 and bf16. That spares the first pass its 128
+// products and scale loads. Elsewhere, and in masked tiles, the exact
+// maximum. Strict like the 16-bit rows' functions.
 template <bool kMasked>
-__device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* ksc, const float* vsc, uint64_t mw0,
-                                                     uint64_t mw1, float& m_run, float& l_run) {
+__device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* ksc, const float* vsc, float top,
+                                                     float low, uint64_t mw0, uint64_t mw1, float& m_run,
+                                                     float& l_run) {
   float mx = -INFINITY;
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-    uint32_t r[32];
-    tmem_ld32(tS + q * 32, r);
-    tmem_wait_ld();
-    const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
-    float a = -INFINITY, b = -INFINITY;
+  bool done = false;
+  if constexpr (!kMasked) {
+    float e0 = -INFINITY, e1 = e0, e2 = e0, e3 = e0;
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      const float4 k4 = *reinterpret_cast<const float4*>(ksc + q * 32 + e);
-      float x0 = __uint_as_float(r[e]) * k4.x, x1 = __uint_as_float(r[e + 1]) * k4.y;
-      float x2 = __uint_as_float(r[e + 2]) * k4.z, x3 = __uint_as_float(r[e + 3]) * k4.w;
-      if constexpr (kMasked) {
-        x0 = (mw >> e) & 1u ? x0 : -INFINITY;
-        x1 = (mw >> (e + 1)) & 1u ? x1 : -INFINITY;
-        x2 = (mw >> (e + 2)) & 1u ? x2 : -INFINITY;
-        x3 = (mw >> (e + 3)) & 1u ? x3 : -INFINITY;
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t s0[32], s1[32];
+      tmem_ld32(tS + 64 * hf, s0);
+      tmem_ld32(tS + 64 * hf + 32, s1);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        e0 = max3nan(e0, __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
+        e1 = max3nan(e1, __uint_as_float(s0[e + 2]), __uint_as_float(s0[e + 3]));
+        e2 = max3nan(e2, __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
+        e3 = max3nan(e3, __uint_as_float(s1[e + 2]), __uint_as_float(s1[e + 3]));
       }
-      a = max3nan(a, x0, x1);
-      b = max3nan(b, x2, x3);
     }
-    mx = max3nan(mx, a, b);
+    const float raw = max3nan(max3nan(e0, e1, e2), e3, e3);
+    done = __all_sync(0xffffffffu, low > 0.f && top <= 4.f * low && fabsf(raw) * top <= 100.f);
+    mx = raw * (raw >= 0.f ? top : low);
+  }
+  if (!done) {
+    mx = -INFINITY;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
+      if (kMasked && !__any_sync(0xffffffffu, mw != 0u)) continue;
+      uint32_t r[32];
+      tmem_ld32(tS + q * 32, r);
+      tmem_wait_ld();
+      float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(ksc + q * 32 + e);
+        float x0 = __uint_as_float(r[e]) * k4.x, x1 = __uint_as_float(r[e + 1]) * k4.y;
+        float x2 = __uint_as_float(r[e + 2]) * k4.z, x3 = __uint_as_float(r[e + 3]) * k4.w;
+        if constexpr (kMasked) {
+          x0 = (mw >> e) & 1u ? x0 : -INFINITY;
+          x1 = (mw >> (e + 1)) & 1u ? x1 : -INFINITY;
+          x2 = (mw >> (e + 2)) & 1u ? x2 : -INFINITY;
+          x3 = (mw >> (e + 3)) & 1u ? x3 : -INFINITY;
+        }
+        a = max3nan(a, x0, x1);
+        b = max3nan(b, x2, x3);
+      }
+      mx = max3nan(mx, a, b);
+    }
   }
   const bool poison = !(mx < INFINITY);
   if (poison) mx = -INFINITY;
@@ -485,24 +521,41 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
   uint64_t acc0 = 0ull, acc1 = 0ull;
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
+    const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
+    uint32_t pk[16];
+    if (kMasked && !__any_sync(0xffffffffu, mw != 0u)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pk[e] = 0u;
+      tmem_st16(tS + q * 16, pk);
+      continue;
+    }
     uint32_t r[32];
     tmem_ld32(tS + q * 32, r);
     tmem_wait_ld();
-    const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
-    uint32_t pk[16];
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
-      const float4 k4 = *reinterpret_cast<const float4*>(ksc + q * 32 + e);
-      const float4 v4 = *reinterpret_cast<const float4*>(vsc + q * 32 + e);
-      float x[4], y[4];
-      f2_unpack(f2_fma(f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), f2_pack(k4.x, k4.y), nm2), x[0], x[1]);
-      f2_unpack(f2_fma(f2_pack(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), f2_pack(k4.z, k4.w), nm2), x[2],
-                x[3]);
+      const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(ksc + q * 32 + e);  // packed pairs
+      const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(vsc + q * 32 + e);
+      const uint64_t x01 = f2_fma(f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), k4.x, nm2);
+      const uint64_t x23 = f2_fma(f2_pack(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), k4.y, nm2);
+      float x[4], z[4];
+      f2_unpack(x01, x[0], x[1]);
+      f2_unpack(x23, x[2], x[3]);
+      uint64_t y01, y23;
+      if constexpr (kMasked) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = !kMasked || ((mw >> (e + i)) & 1u) ? ex2(x[i]) : 0.f;
-      acc0 = f2_add(acc0, f2_pack(y[0], y[1]));
-      acc1 = f2_add(acc1, f2_pack(y[2], y[3]));
-      float z[4] = {y[0] * v4.x, y[1] * v4.y, y[2] * v4.z, y[3] * v4.w};
+        for (int i = 0; i < 4; ++i) x[i] = (mw >> (e + i)) & 1u ? ex2(x[i]) : 0.f;
+        y01 = f2_pack(x[0], x[1]);
+        y23 = f2_pack(x[2], x[3]);
+      } else {
+        y01 = f2_pack(ex2(x[0]), ex2(x[1]));
+        // every fourth pair on the FMA pipe, as in the 16-bit rows
+        y23 = (e & 4) ? exp2_fma2(f2_pack(fmaxf(x[2], -125.f), fmaxf(x[3], -125.f))) : f2_pack(ex2(x[2]), ex2(x[3]));
+      }
+      acc0 = f2_add(acc0, y01);
+      acc1 = f2_add(acc1, y23);
+      f2_unpack(f2_mul(y01, v4.x), z[0], z[1]);
+      f2_unpack(f2_mul(y23, v4.y), z[2], z[3]);
       if constexpr (kMasked) {  // a masked row's scale may hold anything
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = (mw >> (e + i)) & 1u ? z[i] : 0.f;
@@ -571,14 +624,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const uint32_t tmem = ctl->tmem_base;
   // TMEM columns: S/P of half w at 128 w, O of half w at 256 + 128 w.
   wait_for_previous();
-  if constexpr (kQ8) {
-    // 512 threads start with 128 registers each; the softmax warpgroups take
-    // 160 of what the others leave (2 x 96 + 2 x 160 = 4 x 128).
-    if (warp < 4 || warp >= 12)
-      setmaxnreg_dec<96>();
-    else
-      setmaxnreg_inc<160>();
-  }
   Pieces pieces;
   pieces.init(pl);
   Item it;
@@ -600,9 +645,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       uint32_t cls;
       int k = next_seen(it, hv, k0, k1, cls);
       auto page_at = [&](int kk) {  // -2: past the end, -1: outside the pool
-        const int64_t j = (int64_t)it.tile_at(kk) * kPTile + lane * box;
-        if (lane >= boxes || j >= it.s.L) return -2;
-        return (int)page_of(c, it.b, j);
+          const int j = it.tile_at(kk) * kPTile + lane * box;
+          if (lane >= boxes || j >= hv.L) return -2;
+          const int pg = c.table[(int64_t)it.b * c.table_stride + (unsigned)j / (unsigned)c.page_size];
+          if (pg >= 0 && pg < c.num_pages) return pg;
+          set_status(status, ATTN_DEVERR_PAGE);
+          return -1;
       };
       int pg = k < k1 ? page_at(k) : -2;
       while (k < k1) {
@@ -611,7 +659,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const int npg = nk < k1 ? page_at(nk) : -2;
         const int s = n % kPStages;
         const uint32_t info = cls | (nk < k1 ? 16u : 0u) | __ballot_sync(0xffffffffu, pg == -1) << 8;
-        const int off = (int)(((int64_t)it.tile_at(k) * kPTile + lane * box) % c.page_size);
+        const int off = (int)((unsigned)(it.tile_at(k) * kPTile + lane * box) % (unsigned)c.page_size);
         const int page = pg < 0 ? 0 : pg;  // whatever is there: masked, and made finite by the checkers
         if constexpr (!kQ8) {
           ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl->kv_empty[s]), ((n / kPStages) & 1) ^ 1, abort_flag, status));
@@ -782,10 +830,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       // e4m3: thread row of the tile, and its scales one tile ahead.
       const int row = ci * 32 + lane;
       auto scales = [&](int kk) {
-        const int64_t j = (int64_t)it.tile_at(kk) * kPTile + row;
+        const unsigned j = (unsigned)(it.tile_at(kk) * kPTile + row);
         ks_next = vs_next = 0.f;
-        if (j >= it.s.L) return;
-        const int64_t pg = c.table[(int64_t)it.b * c.table_stride + j / c.page_size], o = j % c.page_size;
+        if (j >= (unsigned)hv.L) return;
+        const unsigned e = j / (unsigned)c.page_size, o = j - e * (unsigned)c.page_size;
+        const int pg = c.table[(int64_t)it.b * c.table_stride + e];
         if (pg < 0 || pg >= c.num_pages) return;
         ks_next = c.ks[pg * c.sks[0] + o * c.sks[1] + (int64_t)it.h * c.sks[2]] * (p.scale * kLog2e);
         vs_next = c.vs[pg * c.svs[0] + o * c.svs[1] + (int64_t)it.h * c.svs[2]];
@@ -796,7 +845,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       while (k < k1) {
         const int s = n % kPStages;
         const uint32_t par = (n / kPStages) & 1;
-        const int64_t live = it.s.L - (int64_t)it.tile_at(k) * kPTile;  // rows of the tile inside the sequence
+        const int live = hv.L - it.tile_at(k) * kPTile;  // rows of the tile inside the sequence
         bool part = in_part(cls);
         uint32_t ncls;
         const int nk = next_seen(it, hv, k + 1, k1, ncls);
@@ -843,6 +892,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           float* sc = reinterpret_cast<float*>(smem + M::kScale + s * 1024);
           sc[row] = ks;
           sc[128 + row] = vs;
+          float hi = ks, lo = ks;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            hi = max3nan(hi, __shfl_xor_sync(0xffffffffu, hi, o), hi);
+            lo = min3nan(lo, __shfl_xor_sync(0xffffffffu, lo, o), lo);
+          }
+          if (lane == 0) {
+            ctl->ks_top[s][ci] = hi;
+            ctl->ks_low[s][ci] = lo;
+          }
           auto turn = [&](auto to_fp16, uint32_t raw, uint32_t dst, bool clean) {
             constexpr bool kOutH = decltype(to_fp16)::value;
 #pragma unroll 2
@@ -955,7 +1014,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 
       const int rr = 128 * w + t;
       const bool valid = rr < it.rows;
-      const int64_t pos = it.s.L - it.s.n + (it.row0 + rr) / group;
+      const int pos = hv.L - it.s.n + (it.row0 + rr) / group;
       float m_run = -INFINITY, l_run = 0.f;
       int got = 0;
       uint32_t cls;
@@ -976,8 +1035,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                        : softmax_edge_tile<kH>(tS, sl2, w0, w1, m_run, l_run);
         } else {
           const float* sc = reinterpret_cast<const float*>(smem + M::kScale + s * 1024);
-          alpha = full ? softmax_scaled_tile<false>(tS, sc, sc + 128, w0, w1, m_run, l_run)
-                       : softmax_scaled_tile<true>(tS, sc, sc + 128, w0, w1, m_run, l_run);
+          const float* t4 = ctl->ks_top[s];
+          const float* l4 = ctl->ks_low[s];
+          const float top = max3nan(max3nan(t4[0], t4[1], t4[2]), t4[3], t4[3]);
+          const float low = min3nan(min3nan(l4[0], l4[1], l4[2]), l4[3], l4[3]);
+          alpha = full ? softmax_scaled_tile<false>(tS, sc, sc + 128, top, low, w0, w1, m_run, l_run)
+                       : softmax_scaled_tile<true>(tS, sc, sc + 128, top, low, w0, w1, m_run, l_run);
         }
         if (got > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
