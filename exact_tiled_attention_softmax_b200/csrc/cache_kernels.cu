@@ -4,11 +4,12 @@
 // block table, with the e4m3 form's arithmetic on the way: a row x is stored
 // as s = max|x| / 448 and e4m3(x / s) (448 is e4m3's largest finite value), so
 // a code is off by at most 2^-4 of its value, or by half the smallest
-// subnormal step (2^-10 s) for the smallest entries. Both divisions are the
+// subnormal step (2^-10 s) for the smallest entries. Both quotients are the
 // correctly rounded fp32 ones: multiplying by a rounded 1/s instead moves
 // values that lie on a border between two codes, which 16-bit inputs often do.
 // What bounds them is the bytes: a row is read once and written once, in
-// 16-byte pieces, K and V in the same launch.
+// 16-byte pieces, K and V in the same launch. With a full division per
+// element the write of an 8192-token prompt was bound by instructions.
 #include <math.h>
 
 #include "paged.cuh"
@@ -41,7 +42,27 @@ __device__ __forceinline__ float row_scale(float a) {
 }
 
 // max that keeps a NaN (fmaxf drops it).
-__device__ __forceinline__ float max_nan(float a, float b) { return a != a || b != b ? NAN : fmaxf(a, b); }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// x / s correctly rounded, from the correctly rounded reciprocal r of s: the
+// quotient estimate's exact remainder, times r, corrects it (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990). The remainder is exact while nothing leaves the normal range;
+// callers take it for scales in [2^-90, 2^90], where a quotient that could
+// still round to a nonzero code (at least 2^-11) has a normal remainder.
+// Two quotients in packed fp32.
+__device__ __forceinline__ void quotients(float& x0, float& x1, float s, float r) {
+  asm("{\n\t.reg .b64 x, q, d, ns, rr;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 ns, {%2, %2};\n\tmov.b64 rr, {%3, %3};\n\t"
+      "mul.rn.f32x2 q, x, rr;\n\tfma.rn.f32x2 d, q, ns, x;\n\tfma.rn.f32x2 q, d, rr, q;\n\t"
+      "mov.b64 {%0, %1}, q;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(-s), "f"(r));
+}
 
 template <typename T>
 struct Vec8;  // eight elements as loaded
@@ -59,19 +80,32 @@ struct Vec8<float> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
+  // Largest magnitude; NaN if any element is one.
+  __device__ __forceinline__ float top() const {
+    const float4 p = a, q = b;
+    return max_nan(max_nan(max_nan(fabsf(p.x), fabsf(p.y)), max_nan(fabsf(p.z), fabsf(p.w))),
+                   max_nan(max_nan(fabsf(q.x), fabsf(q.y)), max_nan(fabsf(q.z), fabsf(q.w))));
+  }
   __device__ __forceinline__ void set(const float (&x)[8]) {
     a = make_float4(x[0], x[1], x[2], x[3]);
     b = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
-template <typename T>
+template <typename T2, typename T>
 struct Vec8of16 {
   uint4 u;
+  __device__ __forceinline__ float top() const {  // two elements at a time
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    T2 m = __habs2(*reinterpret_cast<const T2*>(&w[0]));
+#pragma unroll
+    for (int e = 1; e < 4; ++e) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const T2*>(&w[e])));
+    return max_nan(ld(&m.x), ld(&m.y));
+  }
   __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = u; }
 };
 template <>
-struct Vec8<__nv_bfloat16> : Vec8of16<__nv_bfloat16> {
+struct Vec8<__nv_bfloat16> : Vec8of16<__nv_bfloat162, __nv_bfloat16> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -91,7 +125,7 @@ struct Vec8<__nv_bfloat16> : Vec8of16<__nv_bfloat16> {
   }
 };
 template <>
-struct Vec8<__half> : Vec8of16<__half> {
+struct Vec8<__half> : Vec8of16<__half2, __half> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -119,10 +153,10 @@ __device__ __forceinline__ bool slot_of(const CacheP& c, int t, int64_t& pg, int
   const int b = warp_seq_of(c, t);
   if (b < 0) return false;
   const SeqView s = seq_view(c, b);
-  const int64_t pos = s.L - s.n + (t - s.q0);
-  if (pos < 0 || pos >= s.L) return false;
+  const int pos = (int)s.L - s.n + (t - s.q0);
+  if (pos < 0 || pos >= (int)s.L) return false;
   pg = page_of(c, b, pos);
-  off = pos % c.page_size;
+  off = (unsigned)pos % (unsigned)c.page_size;
   return pg >= 0;
 }
 
@@ -132,13 +166,11 @@ __device__ __forceinline__ bool slot_of(const CacheP& c, int t, int64_t& pg, int
 template <typename TS, bool kQuant, int kCh>
 __global__ void __launch_bounds__(256)
 cache_write_vec(CacheP c, const TS* k, int64_t snk0, int64_t snk1, const TS* v, int64_t snv0, int64_t snv1) {
-  if (blockIdx.x == 0) report_ragged(c);
-  const int hblocks = (c.Hkv + kHeadBlock - 1) / kHeadBlock;
-  const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (warp >= (int64_t)c.rows * hblocks) return;
+  if (blockIdx.x == 0 && blockIdx.y == 0) report_ragged(c);
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), h0 = blockIdx.y * kHeadBlock;
+  if (t >= c.rows) return;
   const int lane = threadIdx.x & 31, hl = lane & 15;
   const bool isv = lane >= 16;
-  const int t = (int)(warp / hblocks), h0 = (int)(warp % hblocks) * kHeadBlock;
   const int width = isv ? c.dv : c.d;
   const TS* src = (isv ? v + (int64_t)t * snv0 : k + (int64_t)t * snk0);
   const int64_t sh = isv ? snv1 : snk1;
@@ -165,26 +197,37 @@ cache_write_vec(CacheP c, const TS* k, int64_t snk0, int64_t snk1, const TS* v, 
       float a = 0.f;
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch)
-        if (ch * 128 + hl * 8 < width) {
-          float f[8];
-          x[e][ch].get(f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a = max_nan(a, fabsf(f[i]));
-        }
+        if (ch * 128 + hl * 8 < width) a = max_nan(a, x[e][ch].top());
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));  // within the half-warp
       const float s = row_scale(a);
       uint8_t* dst = const_cast<uint8_t*>(static_cast<const uint8_t*>(isv ? c.v : c.k)) + row;
+      const bool usual = s >= 0x1p-90f && s <= 0x1p90f;  // false for a NaN too
+      const float rs = __frcp_rn(s);
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch)
         if (ch * 128 + hl * 8 < width) {
           float f[8];
           x[e][ch].get(f);
+          if (usual) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) quotients(f[i], f[i + 1], s, rs);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              // one division in the code, for the element that i selects
+              float g = f[0];
+#pragma unroll
+              for (int a = 1; a < 8; ++a) g = i == a ? f[a] : g;
+              g = __fdiv_rn(g, s);
+#pragma unroll
+              for (int a = 0; a < 8; ++a) f[a] = i == a ? g : f[a];
+            }
+          }
           uint32_t w[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            w[i] = (uint32_t)e4m3x2(__fdiv_rn(f[4 * i], s), __fdiv_rn(f[4 * i + 1], s)) |
-                   ((uint32_t)e4m3x2(__fdiv_rn(f[4 * i + 2], s), __fdiv_rn(f[4 * i + 3], s)) << 16);
+            w[i] = (uint32_t)e4m3x2(f[4 * i], f[4 * i + 1]) | ((uint32_t)e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16);
           *reinterpret_cast<uint2*>(dst + ch * 128 + hl * 8) = make_uint2(w[0], w[1]);
         }
       if (hl == 0) {
@@ -239,9 +282,9 @@ template <typename TO, bool kQuant, int kCh>
 __global__ void __launch_bounds__(256)
 cache_read_vec(CacheP c, TO* k, int64_t sk0, int64_t sk1, int64_t sk2, TO* v, int64_t sv0, int64_t sv1, int64_t sv2,
                int T, int jblocks) {
-  const int b = (int)(blockIdx.x / ((int64_t)jblocks * c.Hkv));
-  const int h = (int)((blockIdx.x / jblocks) % c.Hkv);
-  const int j0 = (int)(blockIdx.x % jblocks) * kReadRows;
+  const unsigned bh = blockIdx.x / (unsigned)jblocks;
+  const int b = (int)(bh / (unsigned)c.Hkv), h = (int)(bh % (unsigned)c.Hkv);
+  const int j0 = (int)(blockIdx.x % (unsigned)jblocks) * kReadRows;
   if (blockIdx.x == 0) report_ragged(c);
   const SeqView s = seq_view(c, b);
   const int n = (int)(s.L < T ? s.L : T);
@@ -261,7 +304,7 @@ cache_read_vec(CacheP c, TO* k, int64_t sk0, int64_t sk1, int64_t sk2, TO* v, in
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (pg[e] < 0) continue;
-        const int64_t off = (j0 + g + 16 * e) % c.page_size;
+        const int64_t off = (unsigned)(j0 + g + 16 * e) % (unsigned)c.page_size;
         if (at < c.d) x[e].load(static_cast<const TO*>(c.k) + pg[e] * c.sk[0] + off * c.sk[1] + h * c.sk[2] + at);
         if (at < c.dv) y[e].load(static_cast<const TO*>(c.v) + pg[e] * c.sv[0] + off * c.sv[1] + h * c.sv[2] + at);
       }
@@ -278,7 +321,7 @@ cache_read_vec(CacheP c, TO* k, int64_t sk0, int64_t sk1, int64_t sk2, TO* v, in
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (pg[e] < 0) continue;
-        const int64_t off = (j0 + g + 16 * e) % c.page_size;
+        const int64_t off = (unsigned)(j0 + g + 16 * e) % (unsigned)c.page_size;
         if (at < c.d)
           x[e] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + pg[e] * c.sk[0] + off * c.sk[1] +
                                                  h * c.sk[2] + at);
@@ -355,8 +398,8 @@ cudaError_t write_as(const CacheP& c, const void* kv, const int64_t snk[2], cons
   const TS* k = static_cast<const TS*>(kv);
   const TS* v = static_cast<const TS*>(vv);
   const int e = elem_bytes(src_dtype);
-  if (pool_pieces_ok(c) && pieces_ok(k, snk, 2, c.d, e, 16) && pieces_ok(v, snv, 2, c.dv, e, 16)) {
-    const unsigned g = grid_for((int64_t)c.rows * ((c.Hkv + kHeadBlock - 1) / kHeadBlock));
+  if (pool_pieces_ok(c) && c.Hkv <= 65535 * kHeadBlock && pieces_ok(k, snk, 2, c.d, e, 16) && pieces_ok(v, snv, 2, c.dv, e, 16)) {
+    const dim3 g(grid_for(c.rows), (c.Hkv + kHeadBlock - 1) / kHeadBlock);
     if (c.d <= 128 && c.dv <= 128)
       cache_write_vec<TS, kQuant, 1><<<g, 256, 0, st>>>(c, k, snk[0], snk[1], v, snv[0], snv[1]);
     else

@@ -104,10 +104,10 @@ __device__ __forceinline__ int warp_seq_of(const CacheP& c, int t) {
   return c.cu_q[b] <= t && t < c.cu_q[b + 1] ? b : -1;
 }
 
-// The page that holds position pos of sequence b, or -1 when the table names
+// The page that holds position pos (below 2^30) of sequence b, or -1 when the table names
 // a page outside the pool (reported).
 __device__ __forceinline__ int64_t page_of(const CacheP& c, int b, int64_t pos) {
-  const int64_t pg = c.table[(int64_t)b * c.table_stride + pos / c.page_size];
+  const int64_t pg = c.table[(int64_t)b * c.table_stride + (unsigned)pos / (unsigned)c.page_size];
   if (pg < 0 || pg >= c.num_pages) {
     set_status(c.status, ATTN_DEVERR_PAGE);
     return -1;
