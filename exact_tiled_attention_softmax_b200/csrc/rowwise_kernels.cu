@@ -417,8 +417,10 @@ dsink_reduce(const float* sink, const float* lse, const float* delta, int n_oute
   const float z = sink[h];
   float acc = 0.f;
   const int64_t n = (int64_t)n_outer * n_inner;
+#pragma unroll 4
   for (int64_t r = threadIdx.x; r < n; r += blockDim.x) {
-    const int64_t o = r / n_inner, i = r % n_inner;
+    // a 32-bit quotient where the row number fits one (a 64-bit one takes longer than the rest)
+    const int64_t o = n <= 0xffffffffLL ? (int64_t)((uint32_t)r / (uint32_t)n_inner) : r / n_inner, i = r - o * n_inner;
     const float L = lse[o * sl_outer + h * sl_head + i * sl_inner];
     const int64_t drow = delta_head_major ? (o * n_heads + h) * n_inner + i : (o * n_inner + i) * n_heads + h;
     if (L != -INFINITY) acc += expf(z - L) * delta[drow];

@@ -721,6 +721,15 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
 
 // ------------------------------------------------------------- reverse
 
+// How a reverse launch with first keys shares out its key tiles: the tiles
+// that hold first keys (kt < nft) are seen by every later query and take
+// s_first CTAs each, the others s_rest; the CTAs of a tile take consecutive
+// parts of its steps and leave fp32 partial dK, dV for bwd_join_kernel.
+struct BwdSplit {
+  int nft, s_first, s_rest;
+  float* part;  // [CTAs][dK, dV][32][128 keys] float4
+};
+
 struct BwdArgs {
   MaskP m;
   ClassTable ct;
@@ -736,6 +745,7 @@ struct BwdArgs {
   int64_t sdv[3];
   float scale;
   uint32_t* status;
+  BwdSplit sp;  // read by the split instantiations only
 };
 
 constexpr uint32_t kHalfQ = kBMb * 64 * 2;  // 8 KB: 64 rows x 64 bf16
@@ -800,15 +810,18 @@ __device__ __forceinline__ void bwd_query_slices(const MaskP& m, int b, int Tq, 
   }
 }
 
-// The next nonempty (query head in group, query slice) after (hh, qs).
+// The next nonempty (query head in group, query slice) after (hh, qs); kSplit:
+// before (h_end, q_end).
+template <bool kSplit>
 __device__ __forceinline__ bool bwd_next_step(const BwdArgs& a, int b, int kvh, int kt, int group, int qs_lo,
-                                              int qs_hi, int& hh, int& qs, uint8_t& cls) {
+                                              int qs_hi, int h_end, int q_end, int& hh, int& qs, uint8_t& cls) {
   if (qs_lo > qs_hi) return false;
   while (true) {
     if (++qs > qs_hi) {
       if (++hh >= group) return false;
       qs = qs_lo;
     }
+    if (kSplit && (hh > h_end || (hh == h_end && qs >= q_end))) return false;
     cls = lookup_class(a.ct, a.m, a.Tq, a.Tk, b, kvh * group + hh, qs, kt);
     if (cls != kEmpty) return true;
   }
@@ -961,8 +974,8 @@ __device__ __forceinline__ void bwd_chunk_math(const uint32_t (&rs)[32], const u
 }
 
 // kDQ = false (the deterministic mode) leaves dQ to the query-centric pass:
-// no dQ^T product, no dQ warpgroup work.
-template <bool kH, bool kDQ, bool kDrop>
+// no dQ^T product, no dQ warpgroup work. kSplit: several CTAs per key tile.
+template <bool kH, bool kDQ, bool kDrop, bool kSplit>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
            const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg,
@@ -979,18 +992,35 @@ bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
   // Bands of kBwdBand (b, K/V head) pairs: within a band the earliest key tiles
   // (most work under a causal mask) go first; the CTAs resident at any time
   // then share a few heads' dQ accumulator rows and Q/dO in L2.
-  const int nkt_all = (a.Tk + kBN - 1) / kBN;
+  int nkt_all = (a.Tk + kBN - 1) / kBN;
+  if constexpr (kSplit) nkt_all = a.sp.nft * a.sp.s_first + (nkt_all - a.sp.nft) * a.sp.s_rest;
   const int nbkv = a.B * a.Hkv;
   const int band = (int)(blockIdx.x / ((int64_t)kBwdBand * nkt_all));
   const int band0 = band * kBwdBand;
   const int bw = nbkv - band0 < kBwdBand ? nbkv - band0 : kBwdBand;
   const int within = (int)(blockIdx.x - (int64_t)band0 * nkt_all);
-  const int kt = within / bw;
+  int kt = within / bw;
+  int share = 0, shares = 1;  // this CTA's part of the tile's steps
+  if constexpr (kSplit) {
+    const int at = kt - a.sp.nft * a.sp.s_first;
+    shares = at < 0 ? a.sp.s_first : a.sp.s_rest;
+    share = at < 0 ? kt % shares : at % shares;
+    kt = at < 0 ? kt / shares : a.sp.nft + at / shares;
+  }
   const int bkv = band0 + within % bw;
   const int kvh = bkv % a.Hkv, b = bkv / a.Hkv;
   const int k0 = kt * kBN;
   int qs_lo, qs_hi;
   bwd_query_slices(a.m, b, a.Tq, k0, qs_lo, qs_hi);
+  int h_first = 0, q_first = qs_lo - 1, h_end = group, q_end = qs_lo;
+  if constexpr (kSplit) {
+    const int nq = qs_hi >= qs_lo ? qs_hi - qs_lo + 1 : 1, all = group * nq;  // at most Hq * Tq / 64
+    const int lo = (int)((int64_t)share * all / shares), hi = (int)((int64_t)(share + 1) * all / shares);
+    h_first = lo / nq;
+    q_first = qs_lo + lo % nq - 1;
+    h_end = hi / nq;
+    q_end = qs_lo + hi % nq;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ctl->kv_full), 1);
@@ -1035,15 +1065,15 @@ bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
     tma_load_4d(sbase + kBwdV + kTileBytes / 2, &tv, kvf, 64, k0, kvh, b);
     // The step walk (query head, query slice, class) runs here, ahead of the
     // MMA issuer and the compute warpgroups, which read it from qinfo.
-    int n = 0, hh = 0, qs = qs_lo - 1;
+    int n = 0, hh = h_first, qs = q_first;
     uint8_t cls, ncls = 0;
-    bool have = bwd_next_step(a, b, kvh, kt, group, qs_lo, qs_hi, hh, qs, cls);
+    bool have = bwd_next_step<kSplit>(a, b, kvh, kt, group, qs_lo, qs_hi, h_end, q_end, hh, qs, cls);
     int nh = hh, nq = qs;
-    bool next = have && bwd_next_step(a, b, kvh, kt, group, qs_lo, qs_hi, nh, nq, ncls);
+    bool next = have && bwd_next_step<kSplit>(a, b, kvh, kt, group, qs_lo, qs_hi, h_end, q_end, nh, nq, ncls);
     while (have) {
       int mh = nh, mq = nq;
       uint8_t mcls = 0;
-      const bool next2 = next && bwd_next_step(a, b, kvh, kt, group, qs_lo, qs_hi, mh, mq, mcls);
+      const bool next2 = next && bwd_next_step<kSplit>(a, b, kvh, kt, group, qs_lo, qs_hi, h_end, q_end, mh, mq, mcls);
       const int h = kvh * group + hh;
       const int s = n % kQStages;
       if (!wait_bar(smem_u32(&ctl->q_empty[s]), ((n / kQStages) & 1) ^ 1, abort_flag, a.status)) break;
@@ -1129,9 +1159,9 @@ bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
       __syncwarp();
       return true;
     };
-    int hh0 = 0, qs0 = qs_lo - 1, n = 0;
+    int hh0 = h_first, qs0 = q_first, n = 0;
     uint8_t cls0;
-    bool have = ok && bwd_next_step(a, b, kvh, kt, group, qs_lo, qs_hi, hh0, qs0, cls0);
+    bool have = ok && bwd_next_step<kSplit>(a, b, kvh, kt, group, qs_lo, qs_hi, h_end, q_end, hh0, qs0, cls0);
     uint32_t info = 0;
     if (have) ok = issue_st(0, info);
     while (ok && have) {
@@ -1190,10 +1220,10 @@ bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
     bool ok = true;
     bool any, mine;  // the CTA has a step; this warpgroup's next step exists
     {
-      int hh0 = 0, qs0 = qs_lo - 1;
+      int hh0 = h_first, qs0 = q_first;
       uint8_t cls0;
-      any = bwd_next_step(a, b, kvh, kt, group, qs_lo, qs_hi, hh0, qs0, cls0);
-      mine = any && (!kAlt || w == 0 || bwd_next_step(a, b, kvh, kt, group, qs_lo, qs_hi, hh0, qs0, cls0));
+      any = bwd_next_step<kSplit>(a, b, kvh, kt, group, qs_lo, qs_hi, h_end, q_end, hh0, qs0, cls0);
+      mine = any && (!kAlt || w == 0 || bwd_next_step<kSplit>(a, b, kvh, kt, group, qs_lo, qs_hi, h_end, q_end, hh0, qs0, cls0));
     }
     for (int n = kAlt ? w : 0; ok && mine; n += kAlt ? 2 : 1) {
       const int s = n & 1, sq = n % kQStages;
@@ -1256,7 +1286,25 @@ bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
       have = ok;
     }
     const float osc = w == 0 ? a.scale : (a.m.dropout ? a.m.inv_keep : 1.f);
-    if (ok) {
+    if (kSplit && shares > 1) {
+      float4* part = reinterpret_cast<float4*>(a.sp.part) + ((size_t)bkv * nkt_all + within / bw) * (2 * 32 * kBN) +
+                     w * 32 * kBN + t;
+      const uint32_t tacc = (w == 0 ? tDK : tDV) + lane_off;
+#pragma unroll 1
+      for (int c = 0; c < 4 && ok; ++c) {
+        uint32_t r[32];
+        if (have) {
+          tmem_ld32(tacc + c * 32, r);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          part[(c * 8 + e) * kBN] =
+              have ? make_float4(__uint_as_float(r[4 * e]) * osc, __uint_as_float(r[4 * e + 1]) * osc,
+                                 __uint_as_float(r[4 * e + 2]) * osc, __uint_as_float(r[4 * e + 3]) * osc)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    } else if (ok) {
       uint16_t* orow = w == 0 ? a.dk + b * a.sdk[0] + kvh * a.sdk[1] + j * a.sdk[2]
                               : a.dv + b * a.sdv[0] + kvh * a.sdv[1] + j * a.sdv[2];
       const uint32_t tacc = (w == 0 ? tDK : tDV) + lane_off;
@@ -1291,10 +1339,10 @@ bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
     const uint32_t stage_s = sbase + kBwdDQ + wq * (kBMb * 32 * 4);
     float* stage = reinterpret_cast<float*>(smem + kBwdDQ + wq * (kBMb * 32 * 4));
     if (lane == 0) tma_prefetch_desc(&tdq);
-    int n = 0, hh = 0, qs = qs_lo - 1;
+    int n = 0, hh = h_first, qs = q_first;
     uint8_t cls;
     bool ok = true;
-    while (ok && bwd_next_step(a, b, kvh, kt, group, qs_lo, qs_hi, hh, qs, cls)) {
+    while (ok && bwd_next_step<kSplit>(a, b, kvh, kt, group, qs_lo, qs_hi, h_end, q_end, hh, qs, cls)) {
       const int h = kvh * group + hh;
       const int s = n & 1;
       if (!(ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl->dq_full[s]), (n >> 1) & 1, abort_flag, a.status))))
@@ -1332,6 +1380,38 @@ bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// dK and dV of the key tiles that several CTAs shared: their partial sums added
+// in the CTAs' order. Block (key tile, b and K/V head, kJoinThreads of the
+// tile's 8192 groups of four); a lane per key.
+constexpr int kJoinThreads = 512;
+
+template <bool kH>
+__global__ void __launch_bounds__(kJoinThreads) bwd_join_kernel(const BwdArgs a) {
+  const int kt = blockIdx.x, bkv = blockIdx.y;
+  const int shares = kt < a.sp.nft ? a.sp.s_first : a.sp.s_rest;
+  if (shares == 1) return;
+  const int nkt = (a.Tk + kBN - 1) / kBN, per = a.sp.nft * a.sp.s_first + (nkt - a.sp.nft) * a.sp.s_rest;
+  const int u0 = kt < a.sp.nft ? kt * a.sp.s_first : a.sp.nft * a.sp.s_first + (kt - a.sp.nft) * a.sp.s_rest;
+  const int kvh = bkv % a.Hkv, b = bkv / a.Hkv;
+  const int e = blockIdx.z * kJoinThreads + threadIdx.x;
+  const int w = e / (32 * kBN), c4 = (e / kBN) % 32, t = e % kBN;
+  const int64_t j = (int64_t)kt * kBN + t;
+  if (j >= a.Tk) return;
+  const float4* p = reinterpret_cast<const float4*>(a.sp.part) + ((size_t)bkv * per + u0) * (2 * 32 * kBN) + e;
+  float4 s = p[0];
+#pragma unroll 4
+  for (int i = 1; i < shares; ++i) {
+    const float4 x = p[(size_t)i * (2 * 32 * kBN)];
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  }
+  uint16_t* out = w == 0 ? a.dk + b * a.sdk[0] + kvh * a.sdk[1] + j * a.sdk[2]
+                         : a.dv + b * a.sdv[0] + kvh * a.sdv[1] + j * a.sdv[2];
+  *reinterpret_cast<uint2*>(out + 4 * c4) = make_uint2(pack16<kH>(s.x, s.y), pack16<kH>(s.z, s.w));
 }
 
 // ---------------------------------------------- deterministic dQ (query-centric)
@@ -1829,12 +1909,50 @@ bool tma_ok(const attn_tensor* t) {
   return true;
 }
 
+// The CTAs of a reverse launch, and their partial sums' bytes. A tile with
+// first keys takes a step for every query slice of the sequence, the others
+// only for the window's, so that its CTA alone can outlast the rest of the
+// launch (with few heads), and a short sequence has fewer tiles than the GPU
+// SMs. Split where the longest tile has over half of an SM's average steps:
+// into shares of half that average, or, where the average is below a window
+// tile's steps, as many shares as fill the SMs once. B=2, 16/4 heads, T=1000,
+// window 256: reverse kernel 110 us unsplit, 38 us split; with 32/32 heads at
+// T=8192 (average 286 steps, longest 128) splitting buys nothing.
+BwdSplit bwd_split(int B, int Hq, int Hkv, int Tq, int Tk, uint32_t flags, int64_t window, int64_t first,
+                   bool dropout) {
+  BwdSplit sp{0, 1, 1, nullptr};
+  if (!(flags & ATTN_MASK_FIRST) || first <= 0 || dropout || Tq < 1 || Tk < 1) return sp;
+  constexpr int64_t kSms = 148, kLeast = 8;  // fewest steps worth a CTA's set-up and its partial sums
+  const int64_t nkt = (Tk + kBN - 1) / kBN, nq = (Tq + kBMb - 1) / kBMb, group = Hq / Hkv, bkv = (int64_t)B * Hkv;
+  const int64_t nft = first < Tk ? (first + kBN - 1) / kBN : nkt;
+  const int64_t span = window < Tq ? (window + kBN + kBMb - 2) / kBMb + 1 : nq;
+  const int64_t n_first = group * nq, n_rest = group * (span < nq ? span : nq);
+  const int64_t avg = bkv * (nft * n_first + (nkt - nft) * n_rest) / kSms + 1;
+  if (2 * n_first <= avg) return sp;
+  auto shares = [](int64_t n, int64_t each) { return n > each + each / 2 ? (n + each - 1) / each : 1; };
+  auto ctas = [&](int64_t each) { return bkv * (nft * shares(n_first, each) + (nkt - nft) * shares(n_rest, each)); };
+  int64_t each = avg >= n_rest ? avg / 2 : avg;
+  if (each < kLeast) each = kLeast;
+  if (avg < n_rest)
+    while (ctas(each) > kSms && each < n_first) ++each;
+  sp.nft = (int)nft;
+  sp.s_first = (int)shares(n_first, each);
+  sp.s_rest = (int)shares(n_rest, each);
+  return sp;
+}
+
+size_t bwd_split_bytes(const BwdSplit& sp, int B, int Hkv, int Tk) {
+  if (sp.s_first == 1 && sp.s_rest == 1) return 0;
+  const size_t nkt = (Tk + kBN - 1) / kBN;
+  return (size_t)B * Hkv * (sp.nft * sp.s_first + (nkt - sp.nft) * sp.s_rest) * (2 * kBN * kD * sizeof(float));
+}
+
 // Raise a kernel's dynamic shared-memory limit once per device. which names
 // the kernel instantiation, one slot each: forward 0-3, query-centric dQ 4-5,
-// reverse 8-15.
+// reverse 8-15, split reverse 16-19.
 cudaError_t set_smem_attr(const void* fn, uint32_t bytes, int which) {
-  static bool done[16][64] = {};
-  if (which < 0 || which >= 16) return cudaErrorInvalidValue;
+  static bool done[20][64] = {};
+  if (which < 0 || which >= 20) return cudaErrorInvalidValue;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1862,6 +1980,11 @@ size_t class_bytes(int B, int Hq, int Tq, int Tk, const attn_mask* m) {
   return align_up((size_t)nb * nh * nqs * nkt, 256);
 }
 
+// Bytes that the table takes in the workspace (class_bytes, from the table).
+size_t class_table_bytes(const ClassTable& ct, uint32_t flags) {
+  return flags & kTableFlags ? align_up((size_t)ct.nb * ct.nh * ct.nqs * ct.nkt, 256) : 0;
+}
+
 ClassTable build_class_table(const DenseP& p, void* ws, cudaStream_t st, cudaError_t& err) {
   ClassTable ct;
   ct.cls = nullptr;
@@ -1887,9 +2010,12 @@ size_t sm100_fwd_workspace_bytes(int B, int Hq, int Tq, int Tk, const attn_mask*
 }
 
 size_t sm100_bwd_extra_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, const attn_mask* m) {
-  (void)Hkv;
   const size_t Tpad = (size_t)((Tq + kBN - 1) / kBN) * kBN;
-  return 2 * align_up((size_t)B * Hq * Tpad * sizeof(float), 256) + class_bytes(B, Hq, Tq, Tk, m);
+  const size_t split = m && (m->flags & ATTN_MASK_FIRST)
+                           ? bwd_split_bytes(bwd_split(B, Hq, Hkv, Tq, Tk, m->flags, m->window_left, m->window_first,
+                                                       m->dropout_p > 0.f), B, Hkv, Tk)
+                           : 0;
+  return 2 * align_up((size_t)B * Hq * Tpad * sizeof(float), 256) + class_bytes(B, Hq, Tq, Tk, m) + split;
 }
 
 bool sm100_dense_supported(const DenseP& p, const attn_tensor* q, const attn_tensor* k, const attn_tensor* v,
@@ -2000,19 +2126,32 @@ cudaError_t sm100_dense_bwd(const DenseP& p, const void* o, const int64_t so[3],
   const bool drop = p.m.dropout != 0;
   using BwdFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
                          const CUtensorMap, const BwdArgs);
-  // [fp16][no dQ][dropout]
-  const BwdFn table[2][2][2] = {{{bwd_kernel<false, true, false>, bwd_kernel<false, true, true>},
-                                 {bwd_kernel<false, false, false>, bwd_kernel<false, false, true>}},
-                                {{bwd_kernel<true, true, false>, bwd_kernel<true, true, true>},
-                                 {bwd_kernel<true, false, false>, bwd_kernel<true, false, true>}}};
-  auto kern = table[f16][det][drop];
-  const int which = 8 + (f16 ? 4 : 0) + (det ? 2 : 0) + (drop ? 1 : 0);  // 8 .. 15
-  if ((err = set_smem_attr(reinterpret_cast<const void*>(kern), kBwdSmem, which)) != cudaSuccess) return err;
+  // [fp16][no dQ][dropout], and [fp16][no dQ] of the split form
+  const BwdFn table[2][2][2] = {
+      {{bwd_kernel<false, true, false, false>, bwd_kernel<false, true, true, false>},
+       {bwd_kernel<false, false, false, false>, bwd_kernel<false, false, true, false>}},
+      {{bwd_kernel<true, true, false, false>, bwd_kernel<true, true, true, false>},
+       {bwd_kernel<true, false, false, false>, bwd_kernel<true, false, true, false>}}};
+  const BwdFn split_table[2][2] = {{bwd_kernel<false, true, false, true>, bwd_kernel<false, false, false, true>},
+                                   {bwd_kernel<true, true, false, true>, bwd_kernel<true, false, false, true>}};
   const int nkt = (p.Tk + kBN - 1) / kBN;
+  a.sp = bwd_split(p.B, p.Hq, p.Hkv, p.Tq, p.Tk, p.m.first ? ATTN_MASK_FIRST : 0u, p.m.window, p.m.first, drop);
+  const bool split = a.sp.s_first > 1 || a.sp.s_rest > 1;
+  a.sp.part = reinterpret_cast<float*>(static_cast<char*>(ws_extra) + 2 * padb +
+                                       class_table_bytes(ct, p.m.flags));
+  const int ctas = a.sp.nft * a.sp.s_first + (nkt - a.sp.nft) * a.sp.s_rest;  // nkt where nothing is split
+  auto kern = split ? split_table[f16][det] : table[f16][det][drop];
+  const int which = split ? 16 + (f16 ? 2 : 0) + (det ? 1 : 0) : 8 + (f16 ? 4 : 0) + (det ? 2 : 0) + (drop ? 1 : 0);
+  if ((err = set_smem_attr(reinterpret_cast<const void*>(kern), kBwdSmem, which)) != cudaSuccess) return err;
   main_kernel_begin(st);
-  kern<<<nkt * p.B * p.Hkv, kBwdThreads, kBwdSmem, st>>>(mq, mk, mv, mg, mdq, a);
+  kern<<<ctas * p.B * p.Hkv, kBwdThreads, kBwdSmem, st>>>(mq, mk, mv, mg, mdq, a);
   main_kernel_end(st);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  if (split) {
+    (f16 ? bwd_join_kernel<true> : bwd_join_kernel<false>)<<<dim3(nkt, p.B * p.Hkv, 2 * 32 * kBN / kJoinThreads),
+                                                                  kJoinThreads, 0, st>>>(a);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  }
   if (p.bwd_flags & ATTN_BWD_DETERMINISTIC) {
     // dQ from the query-centric pass: one CTA sums each element in key order.
     CUtensorMap dq_mq, dq_mg;
