@@ -613,8 +613,11 @@ attn_status attn_bwd(const attn_tensor* q, const attn_tensor* k, const attn_tens
     sl[2] = 1;
   }
   if (sm100_dense_supported(p, q, k, v, o) && sm100_dense_bwd_supported(p, do_, dq, dk, dv)) {
+    // With first keys the sink gradient sums an fp32 delta; without, the
+    // product with the stored 16-bit O, whose rounding leaves it off by about
+    // 1e-3 of the terms' size.
     e = sm100_dense_bwd(p, o->data, so, do_->data, sg, lsep, sl, delta, dq_acc, dq->data, sdq, dk->data, sdk,
-                        dv->data, sdv, extra, status, cs);
+                        dv->data, sdv, extra, want_dsink && p.m.first > 0, status, cs);
   } else {
     e = by_storage(q->dtype, [&](auto t) {
       using T = decltype(t);

@@ -424,7 +424,9 @@ __device__ __forceinline__ float softmax_full_tile_drop(uint32_t tS, float scale
 // into the warpgroup's own S columns of TMEM and read from there by the PV
 // MMA; S of the next tile lands in the same columns only after that PV, in
 // issue order.
-template <bool kH, bool kDrop>
+// kFirst (a window with first keys): exponentials accurate to 3e-6, since that
+// form's sink gradient is carried to fp32 accuracy through the LSE.
+template <bool kH, bool kDrop, bool kFirst>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
            const __grid_constant__ CUtensorMap tv, const FwdArgs a) {
@@ -644,7 +646,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
       float alpha;
       if (cls == kFull)
         alpha = kDrop ? softmax_full_tile_drop<kH>(tS, a.scale_log2, m_run, l_run, kb0, kb1)
-                      : softmax_full_tile<kH, kDrop>(tS, a.scale_log2, m_run, l_run, kb0, kb1);
+                      : softmax_full_tile<kH, kDrop, kFirst>(tS, a.scale_log2, m_run, l_run, kb0, kb1);
       else
         alpha = softmax_masked_tile<kH>(tS, a.scale_log2, mw0, mw1, kb0, kb1, m_run, l_run);
       // Every earlier P V of this warpgroup has completed (the S commit covers
@@ -1439,6 +1441,7 @@ struct DqArgs {
   int64_t sdq[3];
   float scale;
   int Tpad;
+  float* rowsum;         // [B*Hq, Tq] (kSum): sum over the keys of p_ij dP_ij
 };
 
 constexpr uint32_t kDqQ = 0;                              // Q tile
@@ -1469,7 +1472,9 @@ __device__ __forceinline__ int dq_next_tile(const FwdArgs& a, int b, int h, int 
   return kt_hi + 1;
 }
 
-template <bool kH>
+// kSum: each row's delta_i = sum_j p_ij <G_i, V_j> as well, in fp32 (the
+// prepare kernel's <G_i, Y_i> takes the stored, 16-bit Y).
+template <bool kH, bool kSum>
 __global__ void __launch_bounds__(kDqThreads, 1)
 dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg, const DqArgs a) {
@@ -1633,6 +1638,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     const int slice = 2 * qt + ((warp & 3) >> 1);               // this warp's 64-row slice
     const uint64_t sc2 = f2_pack(f.scale_log2, f.scale_log2), nl2 = f2_pack(nlse2, nlse2);
     const uint64_t nd2 = f2_pack(ndelta, ndelta);
+    float dsum = 0.f;  // this warpgroup's columns of sum_j p dP
     int n = 0;
     bool ok = true;
     // Tile classes, 32 key tiles per round: lane l holds tile cbase + l
@@ -1708,6 +1714,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int c0 = 32 * hh + 2 * e;
+            if constexpr (kSum) {
+              dsum = fmaf(p[c0], __uint_as_float(r[2 * e]), dsum);
+              dsum = fmaf(p[c0 + 1], __uint_as_float(r[2 * e + 1]), dsum);
+            }
             const uint64_t g2 = f2_mul(f2_pack(p[c0], p[c0 + 1]),
                                        f2_add(f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), nd2));
             float g0, g1;
@@ -1720,6 +1730,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
             const int c0 = 32 * hh + 2 * e, c1 = c0 + 1;
             const float d0 = ((kw >> c0) & 1ull) ? __uint_as_float(r[2 * e]) * dscale : 0.f;
             const float d1 = ((kw >> c1) & 1ull) ? __uint_as_float(r[2 * e + 1]) * dscale : 0.f;
+            if constexpr (kSum) dsum = fmaf(p[c0], d0, fmaf(p[c1], d1, dsum));
             pk[e] = pack16<kH>(p[c0] * (d0 + ndelta), p[c1] * (d1 + ndelta));
           }
         }
@@ -1762,9 +1773,17 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         }
       }
     }
+    // Every product has read the Q tile by now (dq_final, or there was none).
+    if constexpr (kSum) reinterpret_cast<float*>(smem + kDqQ)[w * kBM + t] = ok ? dsum : 0.f;
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kSum) {
+    const int row = q0 + (int)threadIdx.x;
+    const float* part = reinterpret_cast<const float*>(smem + kDqQ);
+    if (threadIdx.x < kBM && row < f.Tq)
+      a.rowsum[((int64_t)b * f.Hq + h) * f.Tq + row] = part[threadIdx.x] + part[kBM + threadIdx.x];
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -1948,11 +1967,11 @@ size_t bwd_split_bytes(const BwdSplit& sp, int B, int Hkv, int Tk) {
 }
 
 // Raise a kernel's dynamic shared-memory limit once per device. which names
-// the kernel instantiation, one slot each: forward 0-3, query-centric dQ 4-5,
-// reverse 8-15, split reverse 16-19.
+// the kernel instantiation, one slot each: forward 0-3 and 6-7 (first keys),
+// query-centric dQ 4-5 and 20-21 (with row sums), reverse 8-15, split 16-19.
 cudaError_t set_smem_attr(const void* fn, uint32_t bytes, int which) {
-  static bool done[20][64] = {};
-  if (which < 0 || which >= 20) return cudaErrorInvalidValue;
+  static bool done[22][64] = {};
+  if (which < 0 || which >= 22) return cudaErrorInvalidValue;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -2064,11 +2083,12 @@ cudaError_t sm100_dense_fwd(const DenseP& p, void* o, const int64_t so[3], float
   a.lse = lse;
   a.status = status;
   const bool drop = p.m.dropout != 0;
-  auto kern = f16 ? (drop ? fwd_kernel<true, true> : fwd_kernel<true, false>)
-                  : (drop ? fwd_kernel<false, true> : fwd_kernel<false, false>);
-  if ((err = set_smem_attr(reinterpret_cast<const void*>(kern), kFwdSmem, (f16 ? 1 : 0) + (drop ? 2 : 0))) !=
-      cudaSuccess)
-    return err;
+  const bool first = p.m.first > 0 && !drop;  // (with dropout every exponential is the hardware's anyway)
+  auto kern = first ? (f16 ? fwd_kernel<true, false, true> : fwd_kernel<false, false, true>)
+              : f16 ? (drop ? fwd_kernel<true, true, false> : fwd_kernel<true, false, false>)
+                    : (drop ? fwd_kernel<false, true, false> : fwd_kernel<false, false, false>);
+  const int which = first ? 6 + (f16 ? 1 : 0) : (f16 ? 1 : 0) + (drop ? 2 : 0);
+  if ((err = set_smem_attr(reinterpret_cast<const void*>(kern), kFwdSmem, which)) != cudaSuccess) return err;
   const int nct = (p.Tq + kFwdRows - 1) / kFwdRows;
   main_kernel_begin(st);
   kern<<<nct * p.B * p.Hq, kFwdThreads, kFwdSmem, st>>>(mq, mk, mv, a);
@@ -2079,7 +2099,7 @@ cudaError_t sm100_dense_fwd(const DenseP& p, void* o, const int64_t so[3], float
 cudaError_t sm100_dense_bwd(const DenseP& p, const void* o, const int64_t so[3], const void* g, const int64_t sg[3],
                             const float* lse, const int64_t sl[3], float* delta, float* dq_acc, void* dq,
                             const int64_t sdq[3], void* dk, const int64_t sdk[3], void* dv, const int64_t sdv[3],
-                            void* ws_extra, uint32_t* status, cudaStream_t st) {
+                            void* ws_extra, bool exact_delta, uint32_t* status, cudaStream_t st) {
   const int Tpad = ((p.Tq + kBN - 1) / kBN) * kBN;
   const size_t padb = align_up((size_t)p.B * p.Hq * Tpad * sizeof(float), 256);
   float* lse2 = static_cast<float*>(ws_extra);
@@ -2088,7 +2108,8 @@ cudaError_t sm100_dense_bwd(const DenseP& p, const void* o, const int64_t so[3],
   ClassTable ct = build_class_table(p, static_cast<char*>(ws_extra) + 2 * padb, st, err);
   if (err != cudaSuccess) return err;
   const bool f16 = p.dtype == ATTN_F16;
-  const bool det = p.bwd_flags & ATTN_BWD_DETERMINISTIC;
+  // The query-centric pass also gives delta in fp32 where it is asked for.
+  const bool det = (p.bwd_flags & ATTN_BWD_DETERMINISTIC) || exact_delta;
   const int64_t rows = (int64_t)p.B * p.Hq * Tpad;  // a multiple of 128: eight rows per warp
   (f16 ? bwd_prepare_kernel<true> : bwd_prepare_kernel<false>)<<<(unsigned)((rows * 4 + 255) / 256), 256, 0, st>>>(
       static_cast<const uint16_t*>(o), so[0], so[1], so[2], static_cast<const uint16_t*>(g), sg[0], sg[1], sg[2], lse,
@@ -2152,7 +2173,7 @@ cudaError_t sm100_dense_bwd(const DenseP& p, const void* o, const int64_t so[3],
                                                                   kJoinThreads, 0, st>>>(a);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
-  if (p.bwd_flags & ATTN_BWD_DETERMINISTIC) {
+  if (det) {
     // dQ from the query-centric pass: one CTA sums each element in key order.
     CUtensorMap dq_mq, dq_mg;
     if (!make_map(&dq_mq, p.q, p.Tq, p.Hq, p.B, p.sq[2], p.sq[1], p.sq[0], kBM, f16) ||
@@ -2178,8 +2199,12 @@ cudaError_t sm100_dense_bwd(const DenseP& p, const void* o, const int64_t so[3],
     for (int i = 0; i < 3; ++i) d.sdq[i] = sdq[i];
     d.scale = p.scale;
     d.Tpad = Tpad;
-    auto kdq = f16 ? dq_kernel<true> : dq_kernel<false>;
-    if ((err = set_smem_attr(reinterpret_cast<const void*>(kdq), kDqSmem, f16 ? 5 : 4)) != cudaSuccess) return err;
+    d.rowsum = exact_delta ? delta : nullptr;
+    auto kdq = exact_delta ? (f16 ? dq_kernel<true, true> : dq_kernel<false, true>)
+                           : (f16 ? dq_kernel<true, false> : dq_kernel<false, false>);
+    if ((err = set_smem_attr(reinterpret_cast<const void*>(kdq), kDqSmem, (exact_delta ? 20 : 4) + (f16 ? 1 : 0))) !=
+        cudaSuccess)
+      return err;
     const int nqt = (p.Tq + kBM - 1) / kBM;
     kdq<<<nqt * p.B * p.Hq, kDqThreads, kDqSmem, st>>>(dq_mq, mk, mv, dq_mg, d);
     return cudaGetLastError();

@@ -550,7 +550,7 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
       } else {
         y01 = f2_pack(ex2(x[0]), ex2(x[1]));
         // every fourth pair on the FMA pipe, as in the 16-bit rows
-        y23 = (e & 4) ? exp2_fma2(f2_pack(fmaxf(x[2], -125.f), fmaxf(x[3], -125.f))) : f2_pack(ex2(x[2]), ex2(x[3]));
+        y23 = (e & 4) ? exp2_pair<true>(fmaxf(x[2], -125.f), fmaxf(x[3], -125.f)) : f2_pack(ex2(x[2]), ex2(x[3]));
       }
       acc0 = f2_add(acc0, y01);
       acc1 = f2_add(acc1, y23);

@@ -386,5 +386,27 @@ __device__ __forceinline__ uint64_t exp2_fma2(uint64_t x) {
                  __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
 }
 
+// The same with a quartic (max relative error 3.1e-6, from the same fit): for
+// sums whose logarithm is an fp32 output.
+__device__ __forceinline__ uint64_t exp2_fma2_fine(uint64_t x) {
+  const uint64_t kRound2 = f2_pack(12582912.0f, 12582912.0f);
+  const uint64_t kNegRound2 = f2_pack(-12582912.0f, -12582912.0f);
+  const uint64_t t = f2_add(x, kRound2);
+  const uint64_t n = f2_add(t, kNegRound2);                  // rint(x)
+  const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);    // x - rint(x), exact
+  uint64_t p = f2_fma(f2_pack(0.00960039533674717f, 0.00960039533674717f), f,
+                      f2_pack(0.05591689422726631f, 0.05591689422726631f));
+  p = f2_fma(p, f, f2_pack(0.24023719131946564f, 0.24023719131946564f));
+  p = f2_fma(p, f, f2_pack(0.6931219696998596f, 0.6931219696998596f));
+  p = f2_fma(p, f, f2_pack(1.0f, 1.0f));
+  // 2^n into the exponent field: the bits of t are 0x4B400000 + n, and
+  // 0x4B400000 << 23 vanishes modulo 2^32, so (bits(t) << 23) = n << 23.
+  float p0, p1, t0, t1;
+  f2_unpack(p, p0, p1);
+  f2_unpack(t, t0, t1);
+  return f2_pack(__uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23)),
+                 __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
+}
+
 }  // namespace sm100
 }  // namespace attn

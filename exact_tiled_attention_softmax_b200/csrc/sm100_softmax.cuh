@@ -46,6 +46,11 @@ __device__ __forceinline__ float move_max(float mx, float& m_run) {
   return alpha;
 }
 
+template <bool kFine>
+__device__ __forceinline__ uint64_t exp2_pair(float x0, float x1) {
+  return kFine ? exp2_fma2_fine(f2_pack(x0, x1)) : exp2_fma2(f2_pack(x0, x1));
+}
+
 // One S row (128 keys, all allowed, no dropout) of the calling thread's TMEM
 // lane -> P (bf16 pairs written over the row's first 64 columns), with the
 // running summary (m_run, l_run) updated. The maximum takes two 64-column
@@ -53,7 +58,7 @@ __device__ __forceinline__ float move_max(float mx, float& m_run) {
 // than 64 scores are live at once (the forward then needs no spill slots);
 // x = s c log2(e) - m is formed on packed fp32 pairs and every kPolyEvery-th
 // pair of exponentials runs on the FMA pipe instead of MUFU. Returns alpha.
-// kStrict: a NaN or +inf score makes l_run NaN (the polynomial and the plain
+// kStrict: the polynomial is the quartic; a NaN or +inf score makes l_run NaN (the polynomial and the plain
 // maximum drop a NaN), and a row of -inf scores adds nothing.
 template <bool kH, bool kDrop, bool kStrict = false>
 __device__ __forceinline__ float softmax_full_tile(uint32_t tS, float scale_log2, float& m_run, float& l_run,
@@ -105,7 +110,7 @@ __device__ __forceinline__ float softmax_full_tile(uint32_t tS, float scale_log2
       float x0, x1;
       f2_unpack(x, x0, x1);
       const uint64_t pp = poly_pair<kDrop>(e)
-                              ? exp2_fma2(f2_pack(fmaxf(x0, -125.f), fmaxf(x1, -125.f)))
+                              ? exp2_pair<kStrict>(fmaxf(x0, -125.f), fmaxf(x1, -125.f))
                               : f2_pack(ex2(x0), ex2(x1));
       if (e & 1)
         acc1 = f2_add(acc1, pp);
