@@ -112,13 +112,6 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t v, uint32_t& lo, uint32_t& h
       : "=r"(lo), "=r"(hi)
       : "r"(v));
 }
-// The same as packed bf16, exact too.
-__device__ __forceinline__ void e4m3x4_bf16(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  e4m3x4_f16(v, lo, hi);
-  const float2 a = unpack16<true>(lo), b = unpack16<true>(hi);
-  lo = pack_bf16(a.x, a.y);
-  hi = pack_bf16(b.x, b.y);
-}
 // One stored element of shared memory as fp32.
 template <bool kHalf>
 __device__ __forceinline__ float ld16(uint32_t addr) {
@@ -155,7 +148,10 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
   constexpr bool kQ8 = R::kQ8;
   constexpr int kRows = 8 * kNT;
   constexpr bool kHalfS = kMode != kBf16;   // K Q^T in fp16 (an e4m3 K is exact in it)
-  constexpr bool kHalfP = kMode == kF16;    // V^T P^T in fp16, else bf16
+  // V^T P^T in fp16 too (e4m3 V is exact in it, and half as many instructions
+  // away as bf16): a probability times its V row's scale has fp16's 2^-11,
+  // and its range is kept by the running reference, below.
+  constexpr bool kHalfP = kMode != kBf16;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ SplitShared ss;
   const CacheP& c = p.c;
@@ -369,12 +365,17 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
         }
         // ---- scale, mask, running summary. Element e: key j0 + g8 + 8 (e >> 1),
         // row 8 nt + 2 t4 + (e & 1).
-        float ksc[2] = {1.f, 1.f}, vsc[2] = {1.f, 1.f};
+        // The running reference m of an e4m3 row is that of s + log2(V's scale),
+        // so that the operand 2^(s - m) scale stays within 2^8 of its
+        // largest value whatever the scales are; the sum takes 2^(s - m)
+        // itself, in fp32. (A scale below 2^-60 counts as 2^-60 there.)
+        float ksc[2] = {1.f, 1.f}, vsc[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
         if constexpr (kQ8) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             ksc[i] = lds32(st + 2 * R::kTileB + (g8 + 8 * i) * 4);
             vsc[i] = lds32(st + 2 * R::kTileB + 64 + (g8 + 8 * i) * 4);
+            lv[i] = fminf(fmaxf(__log2f(fabsf(vsc[i])), -60.f), 120.f);
           }
         }
 #pragma unroll
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(s[nt][e], s[nt][e + 2]);
+            float mx = fmaxf(s[nt][e] + lv[0], s[nt][e + 2] + lv[1]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -496,10 +497,10 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
                 // bytes (w0[2y], w1[2y], w0[2y + 1], w1[2y + 1]): d = .. 2y and 2y + 1 of two keys
                 const uint32_t sel = y ? 0x7362u : 0x5140u;
                 uint32_t a[4];
-                e4m3x4_bf16(__byte_perm(w[0], w[1], sel), a[0], a[1]);
-                e4m3x4_bf16(__byte_perm(w[2], w[3], sel), a[2], a[3]);
+                e4m3x4_f16(__byte_perm(w[0], w[1], sel), a[0], a[1]);
+                e4m3x4_f16(__byte_perm(w[2], w[3], sel), a[2], a[3]);
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) mma16816<false>(acc[nt][2 * q + y], a, pb[nt][0], pb[nt][1]);
+                for (int nt = 0; nt < kNT; ++nt) mma16816<true>(acc[nt][2 * q + y], a, pb[nt][0], pb[nt][1]);
               }
             }
           }

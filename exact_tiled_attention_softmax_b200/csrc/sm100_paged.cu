@@ -11,15 +11,15 @@
 // K/V tiles of 128 keys come page by page: each lane of the producer warp
 // looks up the page of one box of the tile and issues its copies (boxes past the
 // sequence's end or in a page outside the pool take page 0, whose keys are
-// masked). An e4m3 tile lands in a raw buffer, and four
-// warps turn it into the 16-bit operand tile (exact), while the row scales stay
-// fp32: K's multiplies the score, V's the probability.
+// masked). An e4m3 tile lands in a raw buffer, and four warps turn it into the
+// 16-bit operand tiles: K's codes exactly (their scale multiplies the score
+// in fp32), V's times their scales, in fp16.
 //
 // A masked key's V row may hold anything, and 0 times an infinity is not 0.
-// In tiles that some row sees only in part, or that hold such a box, the checker warps (e4m3: the
-// converting ones) therefore take non-finite elements of V out of the operand;
-// rows that do see such a key get them back in the epilogue, where the result is
-// not finite whatever the probability was.
+// In tiles that some row sees only in part, or that hold such a box, the
+// checker warps (e4m3: the converting ones) therefore take non-finite elements
+// of V out of the operand; rows that do see such a key get them back in the
+// epilogue, where the result is not finite whatever the probability was.
 //
 // Work split: plan_kernel lists the blocks of every sequence, deals whole items
 // (block, K/V head) to the CTAs round by round, so that the CTAs walk the same
@@ -318,7 +318,9 @@ struct PagedCtl {
   uint32_t tmem_base;
   uint32_t abort_flag;
   uint32_t odd_piece;  // 1 + the piece whose V tiles lost non-finite elements
-  float ks_top[kPStages][4], ks_low[kPStages][4];  // e4m3: the K scales' extremes, by 32 keys
+  // e4m3, by 32 keys: the K scales' extremes, and the power of two (its
+  // logarithm) that V's scales were divided by.
+  float ks_top[kPStages][4], ks_low[kPStages][4], v_exp[kPStages][4];
   // Per stage: bits 0-3 the halves' classes, bit 4 another tile follows, bits
   // 8-15 boxes in pages outside the pool. raw_info: the same, with the raw K tile.
   uint32_t tinfo[kPStages];
@@ -327,8 +329,8 @@ struct PagedCtl {
 
 template <bool kQ8>
 struct PagedSmem {
-  static constexpr uint32_t kScale = kPRaw + (kQ8 ? 2 * kPRawB : 0);  // kPStages x (128 K, 128 V scales) fp32
-  static constexpr uint32_t kCtl = kScale + (kQ8 ? kPStages * 1024 : 0);
+  static constexpr uint32_t kScale = kPRaw + (kQ8 ? 2 * kPRawB : 0);  // kPStages x 128 K scales, fp32
+  static constexpr uint32_t kCtl = kScale + (kQ8 ? kPStages * 512 : 0);
   static constexpr uint32_t kBytes = kCtl + 512;
   static constexpr int kThreads = kQ8 ? 512 : 384;
   static constexpr int kCheckers = kQ8 ? 4 : 2;  // warps 12-15, or 2 and 3
@@ -450,18 +452,18 @@ __device__ __forceinline__ float softmax_edge_tile(uint32_t tS, float scale_log2
   return alpha;
 }
 
-// The row of an e4m3 tile: scores times the keys' scales (which carry
-// c log2(e)), probabilities times the V rows' scales before they are rounded
-// to bf16. The running summary needs no exact maximum, only a reference m
-// that keeps 2^(x - m) inside fp32's range and never above 2^8 of it: where the
-// tile's K scales lie within a factor of 4 (top, low) and no score passes 100
-// in base 2, the largest unscaled score times `top` (`low`, if it is negative)
-// is above every scaled one by less than 100, and the probabilities keep their
-// relative precision in fp32 and bf16. That spares the first pass its 128
-// products and scale loads. Elsewhere, and in masked tiles, the exact
-// maximum. Strict like the 16-bit rows' functions.
+// The row of an e4m3 tile: scores times the keys' scales ksc (which carry
+// c log2(e)); V's scales are in its operand but for a power of two per 32
+// keys, 2^vexp, which the probabilities take: the running reference m is that
+// of s + vexp, P = 2^(s - m + vexp) in fp16, and the sum 2^(s - m) in fp32.
+// The reference needs no exact maximum: where no score can be further than
+// 16 (in base 2) from the largest unscaled score times `top` (`low`, if it is
+// negative), the tile's extreme K scales, that serves, and spares the first
+// pass its 128 products and scale loads: those loads, 512 bytes of registers
+// per warp and instruction, are what bounds this kernel. Elsewhere, and in
+// masked tiles, the exact maximum. Strict like the 16-bit rows' functions.
 template <bool kMasked>
-__device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* ksc, const float* vsc, float top,
+__device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* ksc, const float* vexp, float top,
                                                      float low, uint64_t mw0, uint64_t mw1, float& m_run,
                                                      float& l_run) {
   float mx = -INFINITY;
@@ -483,8 +485,10 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
       }
     }
     const float raw = max3nan(max3nan(e0, e1, e2), e3, e3);
-    done = __all_sync(0xffffffffu, low > 0.f && top <= 4.f * low && fabsf(raw) * top <= 100.f);
-    mx = raw * (raw >= 0.f ? top : low);
+    const float near = fmaxf(fmaxf(vexp[0], vexp[1]), fmaxf(vexp[2], vexp[3]));
+    const float far = fminf(fminf(vexp[0], vexp[1]), fminf(vexp[2], vexp[3]));
+    done = __all_sync(0xffffffffu, low > 0.f && fabsf(raw) * (top - low) <= 4.f && near - far <= 8.f);
+    mx = raw * (raw >= 0.f ? top : low) + near;
   }
   if (!done) {
     mx = -INFINITY;
@@ -510,15 +514,14 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
         a = max3nan(a, x0, x1);
         b = max3nan(b, x2, x3);
       }
-      mx = max3nan(mx, a, b);
+      mx = max3nan(mx, max3nan(a, b, b) + vexp[q], mx);
     }
   }
   const bool poison = !(mx < INFINITY);
   if (poison) mx = -INFINITY;
   const float alpha = move_max(mx, m_run);
   const float msub = m_run == -INFINITY ? 0.f : m_run;
-  const uint64_t nm2 = f2_pack(-msub, -msub);
-  uint64_t acc0 = 0ull, acc1 = 0ull;
+  float sum = 0.f;
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
     const uint32_t mw = (uint32_t)((q < 2 ? mw0 : mw1) >> (32 * (q & 1)));
@@ -531,14 +534,16 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
     }
     uint32_t r[32];
     tmem_ld32(tS + q * 32, r);
+    const float off = vexp[q] - msub;
+    const uint64_t nm2 = f2_pack(off, off);
+    uint64_t acc0 = 0ull, acc1 = 0ull;
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(ksc + q * 32 + e);  // packed pairs
-      const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(vsc + q * 32 + e);
       const uint64_t x01 = f2_fma(f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), k4.x, nm2);
       const uint64_t x23 = f2_fma(f2_pack(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), k4.y, nm2);
-      float x[4], z[4];
+      float x[4];
       f2_unpack(x01, x[0], x[1]);
       f2_unpack(x23, x[2], x[3]);
       uint64_t y01, y23;
@@ -551,24 +556,21 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
         y01 = f2_pack(ex2(x[0]), ex2(x[1]));
         // every fourth pair on the FMA pipe, as in the 16-bit rows
         y23 = (e & 4) ? exp2_pair<true>(fmaxf(x[2], -125.f), fmaxf(x[3], -125.f)) : f2_pack(ex2(x[2]), ex2(x[3]));
+        f2_unpack(y01, x[0], x[1]);
+        f2_unpack(y23, x[2], x[3]);
       }
       acc0 = f2_add(acc0, y01);
       acc1 = f2_add(acc1, y23);
-      f2_unpack(f2_mul(y01, v4.x), z[0], z[1]);
-      f2_unpack(f2_mul(y23, v4.y), z[2], z[3]);
-      if constexpr (kMasked) {  // a masked row's scale may hold anything
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = (mw >> (e + i)) & 1u ? z[i] : 0.f;
-      }
-      pk[e / 2] = pack_bf16(z[0], z[1]);
-      pk[e / 2 + 1] = pack_bf16(z[2], z[3]);
+      pk[e / 2] = pack_fp16(x[0], x[1]);
+      pk[e / 2 + 1] = pack_fp16(x[2], x[3]);
     }
     tmem_st16(tS + q * 16, pk);
+    float a0, a1, b0, b1;
+    f2_unpack(acc0, a0, a1);
+    f2_unpack(acc1, b0, b1);
+    sum = fmaf((a0 + a1) + (b0 + b1), __uint_as_float((uint32_t)(127 - (int)vexp[q]) << 23), sum);  // 2^-vexp
   }
-  float a0, a1, b0, b1;
-  f2_unpack(acc0, a0, a1);
-  f2_unpack(acc1, b0, b1);
-  l_run = poison ? NAN : l_run * alpha + ((a0 + a1) + (b0 + b1));
+  l_run = poison ? NAN : l_run * alpha + sum;
   return alpha;
 }
 
@@ -595,7 +597,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const CacheP& c = p.c;
   uint32_t* status = c.status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr bool kHP = kH && !kQ8;  // P and V in fp16, else bf16
+  constexpr bool kHP = kH || kQ8;  // P and V in fp16, else bf16
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ctl->q_full), q_boxes ? 1 : 8);
@@ -889,21 +891,33 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           const uint32_t info = ctl->raw_info;
           if (ci == 0 && lane == 0) ctl->tinfo[s] = info;
           part = part || info >> 8 != 0u;
-          float* sc = reinterpret_cast<float*>(smem + M::kScale + s * 1024);
+          float* sc = reinterpret_cast<float*>(smem + M::kScale + s * 512);
           sc[row] = ks;
-          sc[128 + row] = vs;
-          float hi = ks, lo = ks;
+          float hi = ks, lo = ks, ve = isfinite(vs) ? fabsf(vs) : 0.f;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) {
             hi = max3nan(hi, __shfl_xor_sync(0xffffffffu, hi, o), hi);
             lo = min3nan(lo, __shfl_xor_sync(0xffffffffu, lo, o), lo);
+            ve = fmaxf(ve, __shfl_xor_sync(0xffffffffu, ve, o));
           }
+          // V's operand is code (s / 2^e) in fp16, with 2^e the power of two at
+          // or below the 32 rows' largest scale (so below 896), and 2^e goes
+          // to the probabilities' exponents. Rows whose scale is far below the
+          // largest lose bits only where they are below 2^-25 of its rows.
+          const int e2 = min(max((int)(__float_as_uint(ve) >> 23) - 127, -100), 120);
           if (lane == 0) {
             ctl->ks_top[s][ci] = hi;
             ctl->ks_low[s][ci] = lo;
+            ctl->v_exp[s][ci] = (float)e2;
           }
-          auto turn = [&](auto to_fp16, uint32_t raw, uint32_t dst, bool clean) {
-            constexpr bool kOutH = decltype(to_fp16)::value;
+          // vs / 2^e in two steps that stay in range
+          const float vq = vs * __uint_as_float((uint32_t)(127 - e2 / 2) << 23) *
+                           __uint_as_float((uint32_t)(127 - (e2 - e2 / 2)) << 23);
+          const __half2 vh = __float2half2_rn(vq);
+          const uint32_t vscale = *reinterpret_cast<const uint32_t*>(&vh);
+          // kV: V rows (scaled, in fp16); else K rows in the type of Q.
+          auto turn = [&](auto value_rows, uint32_t raw, uint32_t dst, bool clean) {
+            constexpr bool kV = decltype(value_rows)::value, kOutH = kV || kH;
 #pragma unroll 2
             for (int ch = 0; ch < 8; ++ch) {  // 16 codes -> two 16-byte chunks
               const uint4 v = *reinterpret_cast<const uint4*>(smem + raw + sw128_offset(row, ch * 16));
@@ -911,20 +925,28 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               uint32_t o[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                uint32_t x = w[e];
-                if (clean) {
-                  // codes 0x7f and 0xff (NaN) to 0
-                  const uint32_t nan = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                  if (nan) {
-                    x &= ~((nan >> 7) * 0xffu);
-                    odd = odd || row < live;
-                  }
-                }
+                const uint32_t x = w[e];
                 uint32_t h0, h1;
                 asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
                     "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
                     : "=r"(h0), "=r"(h1)
                     : "r"(x));
+                if constexpr (kV) {
+                  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h0) : "r"(vscale));
+                  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h1) : "r"(vscale));
+                  if (clean) {  // non-finite elements to 0
+                    auto finite = [&](uint32_t h) {
+                      const uint32_t f = h & 0x7c007c00u;
+                      uint32_t keep = 0xffffffffu;
+                      if ((f & 0x7c00u) == 0x7c00u) keep &= 0xffff0000u;
+                      if ((f >> 16) == 0x7c00u) keep &= 0x0000ffffu;
+                      odd = odd || (keep != 0xffffffffu && row < live);
+                      return h & keep;
+                    };
+                    h0 = finite(h0);
+                    h1 = finite(h1);
+                  }
+                }
                 if constexpr (kOutH) {
                   o[2 * e] = h0;
                   o[2 * e + 1] = h1;
@@ -940,7 +962,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                   make_uint4(o[4], o[5], o[6], o[7]);
             }
           };
-          turn(Tag<kH>(), kPRaw, kPK + s * kPTileB, false);
+          turn(Tag<false>(), kPRaw, kPK + s * kPTileB, false);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -948,7 +970,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             mbar_arrive(smem_u32(&ctl->raw_empty[0]));
           }
           if (!(ok = wait_all(&ctl->raw_full[1], n & 1))) break;
-          turn(Tag<false>(), kPRaw + kPRawB, kPV + s * kPTileB, part);
+          turn(Tag<true>(), kPRaw + kPRawB, kPV + s * kPTileB, part);
           fence_proxy_async_smem();
         }
         if (__any_sync(0xffffffffu, odd)) {
@@ -1034,13 +1056,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           alpha = full ? softmax_full_tile<kH, false, true>(tS, sl2, m_run, l_run, ~0ull, ~0ull)
                        : softmax_edge_tile<kH>(tS, sl2, w0, w1, m_run, l_run);
         } else {
-          const float* sc = reinterpret_cast<const float*>(smem + M::kScale + s * 1024);
+          const float* sc = reinterpret_cast<const float*>(smem + M::kScale + s * 512);
           const float* t4 = ctl->ks_top[s];
           const float* l4 = ctl->ks_low[s];
           const float top = max3nan(max3nan(t4[0], t4[1], t4[2]), t4[3], t4[3]);
           const float low = min3nan(min3nan(l4[0], l4[1], l4[2]), l4[3], l4[3]);
-          alpha = full ? softmax_scaled_tile<false>(tS, sc, sc + 128, top, low, w0, w1, m_run, l_run)
-                       : softmax_scaled_tile<true>(tS, sc, sc + 128, top, low, w0, w1, m_run, l_run);
+          alpha = full ? softmax_scaled_tile<false>(tS, sc, ctl->v_exp[s], top, low, w0, w1, m_run, l_run)
+                       : softmax_scaled_tile<true>(tS, sc, ctl->v_exp[s], top, low, w0, w1, m_run, l_run);
         }
         if (got > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -1110,9 +1132,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               const int64_t pg = page_of(c, it.b, key);
               if (pg < 0) continue;
               const int64_t at = pg * c.sv[0] + key % c.page_size * c.sv[1] + (int64_t)it.h * c.sv[2] + ch * 32;
+              const float vs = kQ8 ? c.vs[pg * c.svs[0] + key % c.page_size * c.svs[1] + (int64_t)it.h * c.svs[2]] : 1.f;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float v = kQ8 ? ld(static_cast<const __nv_fp8_e4m3*>(c.v) + at + e)
+                const float v = kQ8 ? ld(static_cast<const __nv_fp8_e4m3*>(c.v) + at + e) * vs
                                     : ldf16(static_cast<const uint16_t*>(c.v) + at + e, kH);
                 if (!isfinite(v)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
               }

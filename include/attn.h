@@ -344,9 +344,11 @@ size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, 
  * ATTN_MASK_FIRST, and sink and lse_format; other flags and dropout are
  * ATTN_ERR_UNSUPPORTED. q's dtype is the cache's, or for an ATTN_E4M3 cache any
  * of the other three; o's is q's. Scores take the cached code times its
- * scale exactly (the scale multiplies the fp32 score, and the probability in
- * front of the value row; the tensor-core kernels round that probability to
- * the cache's 16-bit type, to bf16 for an ATTN_E4M3 cache). Infinities and NaN in rows a query does not see
+ * scale exactly (the scale multiplies the fp32 score). The tensor-core kernels
+ * round the probabilities to the cache's 16-bit type, to fp16 for an
+ * ATTN_E4M3 cache, times the value row's scale where max_q asks for the
+ * few-token kernel; the other one takes value rows as fp16(code * scale).
+ * Infinities and NaN in rows a query does not see
  * do not reach it. A row whose allowed scores are all -inf counts as empty.
  * max_q: the largest n_b, if the caller knows it, else 0: it chooses
  * between kernels and never changes which tokens are attended. The result is
