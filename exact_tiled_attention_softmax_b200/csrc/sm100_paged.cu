@@ -456,9 +456,10 @@ __device__ __forceinline__ float softmax_edge_tile(uint32_t tS, float scale_log2
 // c log2(e)); V's scales are in its operand but for a power of two per 32
 // keys, 2^vexp, which the probabilities take: the running reference m is that
 // of s + vexp, P = 2^(s - m + vexp) in fp16, and the sum 2^(s - m) in fp32.
-// The reference needs no exact maximum: where no score can be further than
-// 16 (in base 2) from the largest unscaled score times `top` (`low`, if it is
-// negative), the tile's extreme K scales, that serves, and spares the first
+// The reference needs no exact maximum: where the largest unscaled score times
+// `top` (`low`, if it is negative), the tile's extreme K scales, is above the
+// largest exponent by 8 at most, so that P's largest value is 2^-8 or more and
+// fp16's smallest step 2^-17 of it or less, that serves, and spares the first
 // pass its 128 products and scale loads: those loads, 512 bytes of registers
 // per warp and instruction, are what bounds this kernel. Elsewhere, and in
 // masked tiles, the exact maximum. Strict like the 16-bit rows' functions.
@@ -487,7 +488,7 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
     const float raw = max3nan(max3nan(e0, e1, e2), e3, e3);
     const float near = fmaxf(fmaxf(vexp[0], vexp[1]), fmaxf(vexp[2], vexp[3]));
     const float far = fminf(fminf(vexp[0], vexp[1]), fminf(vexp[2], vexp[3]));
-    done = __all_sync(0xffffffffu, low > 0.f && fabsf(raw) * (top - low) <= 4.f && near - far <= 8.f);
+    done = __all_sync(0xffffffffu, low > 0.f && fabsf(raw) * (top - low) + (near - far) <= 8.f);
     mx = raw * (raw >= 0.f ? top : low) + near;
   }
   if (!done) {
@@ -827,30 +828,37 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     };
     while (ok && pieces.next(p, pl, it, k0, k1, u)) {
       hv.init(p, it);
-      uint32_t cls;
-      float ks_next = 0.f, vs_next = 0.f;
-      // e4m3: thread row of the tile, and its scales one tile ahead.
+      uint32_t cls, ncls;
+      // e4m3: the thread's row of the tile. Its scales are loaded one tile
+      // ahead and the page that holds them two, so that neither is waited for.
       const int row = ci * 32 + lane;
-      auto scales = [&](int kk) {
+      float ks_next = 0.f, vs_next = 0.f;
+      int page_next = -1;
+      auto page_at = [&](int kk) {
         const unsigned j = (unsigned)(it.tile_at(kk) * kPTile + row);
+        if (kk >= k1 || j >= (unsigned)hv.L) return -1;
+        return (int)c.table[(int64_t)it.b * c.table_stride + j / (unsigned)c.page_size];
+      };
+      auto scales = [&](int kk, int pg) {
         ks_next = vs_next = 0.f;
-        if (j >= (unsigned)hv.L) return;
-        const unsigned e = j / (unsigned)c.page_size, o = j - e * (unsigned)c.page_size;
-        const int pg = c.table[(int64_t)it.b * c.table_stride + e];
         if (pg < 0 || pg >= c.num_pages) return;
-        ks_next = c.ks[pg * c.sks[0] + o * c.sks[1] + (int64_t)it.h * c.sks[2]] * (p.scale * kLog2e);
+        const unsigned o = (unsigned)(it.tile_at(kk) * kPTile + row) % (unsigned)c.page_size;
+        ks_next = c.ks[pg * c.sks[0] + o * c.sks[1] + (int64_t)it.h * c.sks[2]];
         vs_next = c.vs[pg * c.svs[0] + o * c.svs[1] + (int64_t)it.h * c.svs[2]];
       };
       int k = next_seen(it, hv, k0, k1, cls);
-      if constexpr (kQ8)
-        if (k < k1) scales(k);
+      int nk = next_seen(it, hv, k + 1, k1, ncls);
+      if constexpr (kQ8) {
+        if (k < k1) scales(k, page_at(k));
+        page_next = page_at(nk);
+      }
       while (k < k1) {
         const int s = n % kPStages;
         const uint32_t par = (n / kPStages) & 1;
         const int live = hv.L - it.tile_at(k) * kPTile;  // rows of the tile inside the sequence
         bool part = in_part(cls);
-        uint32_t ncls;
-        const int nk = next_seen(it, hv, k + 1, k1, ncls);
+        uint32_t nncls;
+        const int nnk = next_seen(it, hv, nk + 1, k1, nncls);
         bool odd = false;
         if constexpr (!kQ8) {
           if (!(ok = wait_all(&ctl->v_full[s], par))) break;
@@ -883,8 +891,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             fence_proxy_async_smem();
           }
         } else {
-          const float ks = ks_next, vs = vs_next;
-          if (nk < k1) scales(nk);
+          const float ks = ks_next * (p.scale * kLog2e), vs = vs_next;
+          scales(nk, page_next);
+          page_next = page_at(nnk);
           // K: wait for the raw tile and for the operand stage
           if (!(ok = wait_all(&ctl->raw_full[0], n & 1))) break;
           if (!(ok = wait_all(&ctl->kv_empty[s], par ^ 1))) break;
@@ -916,36 +925,23 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           const __half2 vh = __float2half2_rn(vq);
           const uint32_t vscale = *reinterpret_cast<const uint32_t*>(&vh);
           // kV: V rows (scaled, in fp16); else K rows in the type of Q.
-          auto turn = [&](auto value_rows, uint32_t raw, uint32_t dst, bool clean) {
+          auto turn = [&](auto value_rows, uint32_t raw, uint32_t dst) {
             constexpr bool kV = decltype(value_rows)::value, kOutH = kV || kH;
-#pragma unroll 2
+#pragma unroll 4
             for (int ch = 0; ch < 8; ++ch) {  // 16 codes -> two 16-byte chunks
               const uint4 v = *reinterpret_cast<const uint4*>(smem + raw + sw128_offset(row, ch * 16));
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
               uint32_t o[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t x = w[e];
                 uint32_t h0, h1;
                 asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
                     "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
                     : "=r"(h0), "=r"(h1)
-                    : "r"(x));
+                    : "r"(w[e]));
                 if constexpr (kV) {
                   asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h0) : "r"(vscale));
                   asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h1) : "r"(vscale));
-                  if (clean) {  // non-finite elements to 0
-                    auto finite = [&](uint32_t h) {
-                      const uint32_t f = h & 0x7c007c00u;
-                      uint32_t keep = 0xffffffffu;
-                      if ((f & 0x7c00u) == 0x7c00u) keep &= 0xffff0000u;
-                      if ((f >> 16) == 0x7c00u) keep &= 0x0000ffffu;
-                      odd = odd || (keep != 0xffffffffu && row < live);
-                      return h & keep;
-                    };
-                    h0 = finite(h0);
-                    h1 = finite(h1);
-                  }
                 }
                 if constexpr (kOutH) {
                   o[2 * e] = h0;
@@ -962,7 +958,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                   make_uint4(o[4], o[5], o[6], o[7]);
             }
           };
-          turn(Tag<false>(), kPRaw, kPK + s * kPTileB, false);
+          turn(Tag<false>(), kPRaw, kPK + s * kPTileB);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -970,7 +966,25 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             mbar_arrive(smem_u32(&ctl->raw_empty[0]));
           }
           if (!(ok = wait_all(&ctl->raw_full[1], n & 1))) break;
-          turn(Tag<true>(), kPRaw + kPRawB, kPV + s * kPTileB, part);
+          turn(Tag<true>(), kPRaw + kPRawB, kPV + s * kPTileB);
+          if (part) {  // the thread's own row again: non-finite elements to 0
+#pragma unroll 1
+            for (int ch = 0; ch < 16; ++ch) {
+              uint32_t* at = reinterpret_cast<uint32_t*>(smem + kPV + s * kPTileB + (ch >> 3) * (kPTileB / 2) +
+                                                         sw128_offset(row, (ch & 7) * 16));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t h = at[e], f = h & 0x7c007c00u;
+                uint32_t keep = 0xffffffffu;
+                if ((f & 0x7c00u) == 0x7c00u) keep &= 0xffff0000u;
+                if ((f >> 16) == 0x7c00u) keep &= 0x0000ffffu;
+                if (keep != 0xffffffffu) {
+                  at[e] = h & keep;
+                  odd = odd || row < live;
+                }
+              }
+            }
+          }
           fence_proxy_async_smem();
         }
         if (__any_sync(0xffffffffu, odd)) {
@@ -987,6 +1001,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         ++n;
         k = nk;
         cls = ncls;
+        nk = nnk;
+        ncls = nncls;
       }
       ++piece;
     }
