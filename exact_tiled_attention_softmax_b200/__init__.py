@@ -551,8 +551,12 @@ def attn_cache_read(cache: PagedCache, max_len: int | None = None, *, dtype=None
     device = cache.k.device
     if k is None or v is None:
         _, page, H, d = cache.k.shape
-        T = int(max_len) if max_len is not None else cache.block_table.shape[1] * page
-        if dtype is None:
+        given = k if k is not None else v
+        T = given.shape[2] if given is not None else \
+            int(max_len) if max_len is not None else cache.block_table.shape[1] * page
+        if given is not None:
+            dtype = given.dtype
+        elif dtype is None:
             dtype = torch.bfloat16 if cache.k.dtype == torch.float8_e4m3fn else cache.k.dtype
         B = cache.seq_lens.shape[0]
         k = torch.zeros(B, H, T, d, dtype=dtype, device=device) if k is None else k

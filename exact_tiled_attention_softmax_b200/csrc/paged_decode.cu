@@ -51,10 +51,12 @@ struct Ring {
   static constexpr int kRowBytes = kQ8 ? kDD : 2 * kDD;
   static constexpr int kTileB = kPiece * kRowBytes;            // one of K, V
   static constexpr int kStageB = 2 * kTileB + (kQ8 ? 128 : 0); // + 16 K scales, 16 V scales
-  static constexpr int kStages = kQ8 ? 3 : 2;
-  // CTAs an SM: what 65536 registers and 227 KB carry (one 8-row e4m3 item's
-  // warps need 128 registers and 50 KB a CTA, the others more of either).
-  static constexpr int kCtas = kQ8 && kNT == 1 ? 4 : 3;
+  static constexpr int kStages = kQ8 ? 4 : 3;
+  // CTAs an SM, against copies in flight per warp (227 KB, 65536 registers):
+  // 64 e4m3 sequences of up to 8192 keys took 159 us with 3 CTAs of 4 stages,
+  // 164 with 4 of 3, 184 with 4 of 2, 190 with 2 of 5; the fp16 window workload
+  // of 32 sequences 35.1 us with 2 of 3, 36.6 with 3 of 2, 51 with 2 of 4.
+  static constexpr int kCtas = kQ8 ? 3 : 2;
   static constexpr int kWarpB = kStages * kStageB;
   static constexpr int kSmem = kDWarps * kWarpB;
   static_assert(kWarpB >= 8 * kNT * (kDD + 2) * 4, "the ring also carries a warp's result to the join");

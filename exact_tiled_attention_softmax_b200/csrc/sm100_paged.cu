@@ -705,16 +705,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         pg = npg;
       }
     }
-    // Every copy lands before the CTA's shared memory goes. (Q's are waited for by
-    // the warp that issues them.)
+    // Every copy lands before the CTA's shared memory goes, aborted or not.
+    uint32_t calm = 0;  // stands in for the abort flag, which would end these waits at once
     if constexpr (!kQ8) {
       for (int r = (n > kPStages ? n - kPStages : 0); r < n; ++r) {
-        wait_bar(smem_u32(&ctl->k_full[r % kPStages]), (r / kPStages) & 1, abort_flag, nullptr);
-        wait_bar(smem_u32(&ctl->v_full[r % kPStages]), (r / kPStages) & 1, abort_flag, nullptr);
+        wait_bar(smem_u32(&ctl->k_full[r % kPStages]), (r / kPStages) & 1, &calm, nullptr);
+        wait_bar(smem_u32(&ctl->v_full[r % kPStages]), (r / kPStages) & 1, &calm, nullptr);
       }
     } else if (n > 0) {
-      wait_bar(smem_u32(&ctl->raw_full[0]), (n - 1) & 1, abort_flag, nullptr);
-      wait_bar(smem_u32(&ctl->raw_full[1]), (n - 1) & 1, abort_flag, nullptr);
+      wait_bar(smem_u32(&ctl->raw_full[0]), (n - 1) & 1, &calm, nullptr);
+      wait_bar(smem_u32(&ctl->raw_full[1]), (n - 1) & 1, &calm, nullptr);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (whole warp; one elected lane issues)
@@ -764,7 +764,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         __syncwarp();
       }
-      if (!(ok = wait_all(&ctl->q_full, piece & 1))) break;
+      if (!(ok = wait_all(&ctl->q_full, piece & 1))) {
+        uint32_t calm = 0;  // Q's copies land before the CTA's shared memory goes
+        if (q_boxes) wait_bar(smem_u32(&ctl->q_full), piece & 1, &calm, nullptr);
+        break;
+      }
       tc_fence_after();
       uint32_t info = 0;
       int npv[2] = {0, 0};

@@ -304,6 +304,92 @@ def test_masked_rows_hold_anything(kind, new, value):
     assert not torch.isfinite(o[~ok.cuda()][:, 70]).any()
 
 
+@pytest.mark.parametrize("kind,new", [("decode", 1), ("few", 4), ("chunk", 150), ("any", 4)])
+def test_masked_e4m3_rows_hold_anything(kind, new):
+    """NaN codes, and scales that are not finite, in e4m3 rows that a query does
+    not see."""
+    page = 7 if kind == "any" else 16
+    L = 290
+    cache, K, V = make_cache([L], page, 2, 128, 128, E4M3, seed=6, src=torch.bfloat16)
+    hit = [100, 289, 270, 288]
+    for j in hit:
+        pg, off = int(cache.block_table[0, j // page]), j % page
+        cache.v.view(torch.uint8)[pg, off, 1, 70] = 0x7F
+        if j == 270:
+            cache.v_scale[pg, off, 1] = math.inf
+        if j == 100:
+            cache.k_scale[pg, off, 1] = math.nan
+    q = seeded_q(new, 4, 128, torch.bfloat16)
+    mask = dict(causal=True, window=16, first=3)
+    o, lse = run(q, cache, [new], allowed=allowed_of(mask), max_q=new)
+    ok = torch.tensor([[h < 2 or not any(p - 16 < j <= p for j in hit) for h in range(4)]
+                       for p in range(L - new, L)])
+    ref = reference(q, K, V, [new], [L], 128 ** -0.5, **mask)
+    check(o[ok.cuda()], lse[ok.cuda()], *[r[ok] for r in ref], tensor_core=True, cache=E4M3)
+    assert not torch.isfinite(o[~ok.cuda()][:, 70]).any()
+
+
+@pytest.mark.parametrize("new,kind", [(1, "decode"), (20, "chunk")])
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+def test_one_long_sequence_is_joined_from_many_shares(new, kind, cd):
+    """One K/V head and one row block: its keys fall to dozens of CTAs."""
+    L = 20011
+    cache, K, V = make_cache([L], 64, 1, 128, 128, DT[cd], seed=12, src=torch.bfloat16)
+    q = seeded_q(new, 4, 128, torch.bfloat16)
+    o, lse = run(q, cache, [new], allowed=eta.AllowedSet(causal=True), max_q=new)
+    check(o, lse, *reference(q, K, V, [new], [L], 128 ** -0.5), tensor_core=True, cache=cd)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 3.0])
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_e4m3_with_other_score_factors(kind, scale):
+    """Negative and zero factors, and one that spreads the scores; row scales
+    that differ by up to 2^12 within a tile, for K and V."""
+    c = ATTN[kind]
+    cache, K, V = make_cache(c["lens"], c["page"], c["Hkv"], 128, 128, E4M3, seed=3, src=torch.bfloat16)
+    g = torch.Generator().manual_seed(9)
+    for b, L in enumerate(c["lens"]):
+        pos = torch.arange(L)
+        at = cache.block_table[b].long().cpu()[pos // c["page"]], pos % c["page"]
+        for sc, dense, most in ((cache.k_scale, K, 3), (cache.v_scale, V, 12)):
+            f = 2.0 ** -torch.randint(0, most + 1, (L, c["Hkv"]), generator=g).double()
+            sc[at[0].cuda(), at[1].cuda()] *= f.float().cuda()
+            dense[b] = dense[b] * f[..., None]
+    q = seeded_q(sum(c["new"]), c["Hq"], 128, torch.bfloat16)
+    o, lse = run(q, cache, c["new"], scale=scale, allowed=eta.AllowedSet(causal=True), max_q=max(c["new"]))
+    o_ref, l_ref, A = reference(q, K, V, c["new"], c["lens"], scale)
+    # Probabilities below fp16's normal range (2^-14 of the row's largest times
+    # scale) are rounded to steps of 2^-24: with N keys, another N 2^-25 of the
+    # largest value row.
+    top = torch.stack([v.abs().amax() for v in V]).max() * max(c["lens"]) * 2.0 ** -25
+    check(o, lse, o_ref, l_ref, A + top * 2.0 ** 9, tensor_core=True, cache=E4M3)
+
+
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_unaligned_tensors(kind, cd):
+    """Rows that start off the 16-byte grid, in q, o or the pool, take the row
+    kernels and give the same answers."""
+    c = ATTN[kind]
+    cache, K, V = make_cache(c["lens"], c["page"], c["Hkv"], 128, 128, DT[cd], src=torch.bfloat16)
+    rows = sum(c["new"])
+    q = seeded_q(rows, c["Hq"], 129, torch.bfloat16)[..., 1:]
+    ref = reference(q, K, V, c["new"], c["lens"], 128 ** -0.5)
+    o, lse = run(q, cache, c["new"], allowed=eta.AllowedSet(causal=True), max_q=max(c["new"]))
+    check(o, lse, *ref, tensor_core=False)
+    out = torch.empty(rows, c["Hq"], 131, dtype=torch.bfloat16, device="cuda")[..., 2:130]
+    run(q, cache, c["new"], allowed=eta.AllowedSet(causal=True), max_q=max(c["new"]), out=out)
+    check(out, lse, *ref, tensor_core=False)
+
+
+def test_read_into_one_given_tensor():
+    cache, K, V = make_cache([33], 16, 2, 128, 128, torch.bfloat16)
+    k = torch.zeros(1, 2, 40, 128, dtype=torch.bfloat16, device="cuda")
+    got_k, got_v = eta.attn_cache_read(cache, k=k)
+    assert got_k is k and got_v.shape == k.shape
+    assert torch.equal(got_v[0, :, :33].transpose(0, 1).double().cpu(), V[0]) and (got_v[0, :, 33:] == 0).all()
+
+
 def test_nan_scores_make_the_row_nan():
     for new, page in ((1, 16), (150, 16), (2, 7)):
         cache, _, _ = make_cache([300], page, 2, 128, 128, torch.bfloat16)

@@ -118,6 +118,32 @@ def test_matches_the_oracle(kind, dtype, deterministic):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_sink_gradient_is_fp32_accurate(dtype):
+    """dz_h = -sum_i p_i delta_i with delta in fp32: each term's error is 2^-18
+    of sum_j p_ij |dP_ij| at most (scores and dP are fp32 sums of 128
+    products, the LSE is off by 4e-6 at most), so the sum's is 2^-18 of the
+    terms' magnitudes."""
+    B, Hq, Hkv, T, W_, F = 2, 4, 2, 700, 96, 5
+    rng = np.random.default_rng(21)
+    f = lambda s: W.round_to_storage(rng.standard_normal(s, dtype=np.float32), dtype)  # noqa: E731
+    q, k, v, g = f((B, Hq, T, 128)), f((B, Hkv, T, 128)), f((B, Hkv, T, 128)), f((B, Hq, T, 128))
+    sink = rng.standard_normal(Hq).astype(np.float32)
+    tq, tk, tv, tg = (to_dev(x, TORCH_DTYPE[dtype]) for x in (q, k, v, g))
+    allowed = eta.AllowedSet(causal=True, window_left=W_, window_first=F, sink=to_dev(sink, torch.float32))
+    o, lse = eta.attn_fwd(tq, tk, tv, allowed)
+    dsink = eta.attn_bwd(tq, tk, tv, o, tg, lse, allowed)[3]
+    allow = allow_grid(T, T, window=W_, first=F)
+    q, k, v, g = (x.astype(np.float64) for x in (q, k, v, g))
+    fw = oracle.forward(q, k, v, allow, 128 ** -0.5, sink=sink.astype(np.float64))
+    bw = oracle.backward(q, k, v, g, allow, 128 ** -0.5, sink=sink.astype(np.float64), y=fw.y)
+    kk, vv = np.repeat(k, Hq // Hkv, 1), np.repeat(v, Hq // Hkv, 1)
+    s = np.where(allow, np.einsum("bhid,bhjd->bhij", q, kk) * 128 ** -0.5, -np.inf)
+    p = np.exp(s - fw.lse[..., None])
+    size = (np.exp(sink[:, None] - fw.lse) * (p * np.abs(np.einsum("bhid,bhjd->bhij", g, vv))).sum(-1)).sum((0, 2))
+    assert (np.abs(to_np(dsink) - bw.dsink) <= 2.0 ** -17 * size).all(), (to_np(dsink) - bw.dsink, size)
+
+
 def test_gradients_against_differences():
     """fp32, autograd: <grad, u> against a central difference along u. With
     h = 2^-6 the difference's own error is h^2/6 times a third derivative

@@ -173,3 +173,31 @@ def test_binding_refuses_host_tensors_and_wrong_tables():
         eta.PagedCache(pool, pool, table.long(), lens).to_c()
     with pytest.raises(ValueError, match="different numbers"):
         eta.PagedCache(pool, pool, table, lens[:1]).to_c()
+
+
+def test_quartic_exponential():
+    """The quartic that stands in for some exponentials where the sum's logarithm
+    is an fp32 output: the kernel's fp32 steps in NumPy, and its coefficients
+    from the generator."""
+    import importlib.util
+
+    import numpy as np
+    path = os.path.join(ROOT, "exact_tiled_attention_softmax_b200", "csrc", "gen_exp2_poly.py")
+    spec = importlib.util.spec_from_file_location("gen_exp2_poly", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    coeffs, err = mod.fit(4)
+    text = open(os.path.join(os.path.dirname(path), "sm100_ptx.cuh")).read()
+    for c in coeffs[1:]:
+        assert f"{float(np.float32(c))!r}f" in text
+    assert err < 3.1e-6
+    x = np.linspace(-120.0, 8.0, 500_001, dtype=np.float32)
+    t = (x + np.float32(12582912.0)).astype(np.float32)
+    f = (x - (t - np.float32(12582912.0))).astype(np.float32)
+    p = np.float32(coeffs[4])
+    for c in coeffs[3::-1]:
+        p = (p * f + np.float32(c)).astype(np.float32)
+    n = t.view(np.int32) - np.int32(0x4B400000)
+    got = (p.view(np.int32) + (n << 23)).view(np.float32).astype(np.float64)
+    # the fit's error, and four roundings of 2^-24 (one is relative to terms below 1)
+    assert np.abs(got / np.exp2(x.astype(np.float64)) - 1).max() < 3.1e-6 + 4 * 2.0 ** -23
