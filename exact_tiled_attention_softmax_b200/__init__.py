@@ -589,9 +589,9 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty((rows, heads, cache.v.shape[3]), dtype=q.dtype, device=device)
+        out = q.new_empty((rows, heads, cache.v.shape[3]))
     if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
+        lse = q.new_empty((rows, heads), dtype=torch.float32)
     m = allowed.to_c() if allowed else None
     cq, c, cu = _tensor(q), cache.to_c(), _cu_q_ptr(cu_q, cache)
     _check_on(device, cache.k, out, lse, workspace, *(allowed.tensors() if allowed else ()))
@@ -601,7 +601,7 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
         if ws is None:
             need = lib.attn_paged_workspace_size(cq, c, m)
             if stream is None:
-                ws = _workspace(need, device)
+                ws = q.new_empty(need, dtype=torch.uint8)
             else:  # from that stream's pool: freed here, reused there after the call
                 with torch.cuda.stream(stream):
                     ws = _workspace(need, device)

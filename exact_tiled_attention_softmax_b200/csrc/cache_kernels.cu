@@ -276,79 +276,90 @@ cache_write_any(CacheP c, const TS* k, int64_t snk0, int64_t snk1, const TS* v, 
 
 constexpr int kReadRows = 64;  // positions a block reads: 16 half-warps x 4 each
 
-// One block per (64 positions, head, sequence). A half-warp reads whole rows,
-// K and V of four positions in flight at once.
+// Two e4m3 codes times a scale, rounded once to the output type.
+template <typename TO>
+__device__ __forceinline__ void scaled8(const uint2& u, float scale, Vec8<TO>& out) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = e4m3x2_to_float2((uint16_t)((i < 2 ? u.x : u.y) >> (16 * (i & 1))));
+    f[2 * i] = p.x * scale;
+    f[2 * i + 1] = p.y * scale;
+  }
+  out.set(f);
+}
+
+// One block per (64 positions, head, sequence), for pages of a multiple of four
+// positions. A half-warp reads the four rows at 4 g of the block, which share
+// a page: one lookup and one address for the four, K and V of all in flight
+// at once. (With a lookup and an address per row the read was bound by
+// instructions: 31.7 us for eight e4m3 sequences of up to 4096.)
 template <typename TO, bool kQuant, int kCh>
 __global__ void __launch_bounds__(256)
 cache_read_vec(CacheP c, TO* k, int64_t sk0, int64_t sk1, int64_t sk2, TO* v, int64_t sv0, int64_t sv1, int64_t sv2,
                int T, int jblocks) {
   const unsigned bh = blockIdx.x / (unsigned)jblocks;
   const int b = (int)(bh / (unsigned)c.Hkv), h = (int)(bh % (unsigned)c.Hkv);
-  const int j0 = (int)(blockIdx.x % (unsigned)jblocks) * kReadRows;
+  const int g = threadIdx.x >> 4, hl = threadIdx.x & 15;
+  const int j = (int)(blockIdx.x % (unsigned)jblocks) * kReadRows + 4 * g;  // the half-warp's first position
   if (blockIdx.x == 0) report_ragged(c);
   const SeqView s = seq_view(c, b);
   const int n = (int)(s.L < T ? s.L : T);
-  if (j0 >= n) return;
-  const int g = threadIdx.x >> 4, hl = threadIdx.x & 15;
-  int64_t pg[4];
+  if (j >= n) return;
+  const int64_t pg = page_of(c, b, j);
+  if (pg < 0) return;
+  const int64_t off = (unsigned)j % (unsigned)c.page_size;
+  const int rows = n - j < 4 ? n - j : 4;
+  float xs[4], ys[4];
+  if constexpr (kQuant) {
+    const float* ks = c.ks + pg * c.sks[0] + off * c.sks[1] + h * c.sks[2];
+    const float* vs = c.vs + pg * c.svs[0] + off * c.svs[1] + h * c.svs[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int j = j0 + g + 16 * e;
-    pg[e] = j < n ? page_of(c, b, j) : -1;
+    for (int e = 0; e < 4; ++e) {
+      xs[e] = e < rows ? ks[e * c.sks[1]] : 0.f;
+      ys[e] = e < rows ? vs[e * c.svs[1]] : 0.f;
+    }
   }
 #pragma unroll
   for (int ch = 0; ch < kCh; ++ch) {
     const int at = ch * 128 + hl * 8;
+    const int64_t kat = pg * c.sk[0] + off * c.sk[1] + h * c.sk[2] + at;
+    const int64_t vat = pg * c.sv[0] + off * c.sv[1] + h * c.sv[2] + at;
+    TO* ko = k + b * sk0 + h * sk1 + j * sk2 + at;
+    TO* vo = v + b * sv0 + h * sv1 + j * sv2 + at;
+    const bool hask = at < c.d, hasv = at < c.dv;
     if constexpr (!kQuant) {
       Vec8<TO> x[4], y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (pg[e] < 0) continue;
-        const int64_t off = (unsigned)(j0 + g + 16 * e) % (unsigned)c.page_size;
-        if (at < c.d) x[e].load(static_cast<const TO*>(c.k) + pg[e] * c.sk[0] + off * c.sk[1] + h * c.sk[2] + at);
-        if (at < c.dv) y[e].load(static_cast<const TO*>(c.v) + pg[e] * c.sv[0] + off * c.sv[1] + h * c.sv[2] + at);
+        if (e < rows && hask) x[e].load(static_cast<const TO*>(c.k) + kat + e * c.sk[1]);
+        if (e < rows && hasv) y[e].load(static_cast<const TO*>(c.v) + vat + e * c.sv[1]);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (pg[e] < 0) continue;
-        const int64_t j = j0 + g + 16 * e;
-        if (at < c.d) x[e].store(k + b * sk0 + h * sk1 + j * sk2 + at);
-        if (at < c.dv) y[e].store(v + b * sv0 + h * sv1 + j * sv2 + at);
+        if (e < rows && hask) x[e].store(ko + e * sk2);
+        if (e < rows && hasv) y[e].store(vo + e * sv2);
       }
     } else {
       uint2 x[4], y[4];
-      float xs[4], ys[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (pg[e] < 0) continue;
-        const int64_t off = (unsigned)(j0 + g + 16 * e) % (unsigned)c.page_size;
-        if (at < c.d)
-          x[e] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + pg[e] * c.sk[0] + off * c.sk[1] +
-                                                 h * c.sk[2] + at);
-        if (at < c.dv)
-          y[e] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + pg[e] * c.sv[0] + off * c.sv[1] +
-                                                 h * c.sv[2] + at);
-        xs[e] = c.ks[pg[e] * c.sks[0] + off * c.sks[1] + h * c.sks[2]];
-        ys[e] = c.vs[pg[e] * c.svs[0] + off * c.svs[1] + h * c.svs[2]];
+        if (e < rows && hask)
+          x[e] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + kat + e * c.sk[1]);
+        if (e < rows && hasv)
+          y[e] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + vat + e * c.sv[1]);
       }
-      auto put = [&](const uint2& u, float scale, TO* dst) {
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 p = e4m3x2_to_float2((uint16_t)((i < 2 ? u.x : u.y) >> (16 * (i & 1))));
-          f[2 * i] = p.x * scale;
-          f[2 * i + 1] = p.y * scale;
-        }
-        Vec8<TO> out;
-        out.set(f);
-        out.store(dst);
-      };
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (pg[e] < 0) continue;
-        const int64_t j = j0 + g + 16 * e;
-        if (at < c.d) put(x[e], xs[e], k + b * sk0 + h * sk1 + j * sk2 + at);
-        if (at < c.dv) put(y[e], ys[e], v + b * sv0 + h * sv1 + j * sv2 + at);
+        Vec8<TO> out;
+        if (e < rows && hask) {
+          scaled8(x[e], xs[e], out);
+          out.store(ko + e * sk2);
+        }
+        if (e < rows && hasv) {
+          scaled8(y[e], ys[e], out);
+          out.store(vo + e * sv2);
+        }
       }
     }
   }
@@ -418,7 +429,7 @@ cudaError_t read_as(const CacheP& c, void* kv, const int64_t sok[3], void* vv, c
   TO* v = static_cast<TO*>(vv);
   const int e = elem_bytes(out_dtype);
   const bool quant = c.dtype == ATTN_E4M3;
-  if (pool_pieces_ok(c) && pieces_ok(k, sok, 3, c.d, e, 16) && pieces_ok(v, sov, 3, c.dv, e, 16)) {
+  if (pool_pieces_ok(c) && c.page_size % 4 == 0 && pieces_ok(k, sok, 3, c.d, e, 16) && pieces_ok(v, sov, 3, c.dv, e, 16)) {
     const int jb = (T + kReadRows - 1) / kReadRows;
     const unsigned g = (unsigned)((int64_t)jb * c.Hkv * c.batch);
     constexpr int kWide = (kMaxWidth + 127) / 128;

@@ -50,7 +50,7 @@ struct Ring {
   static constexpr bool kQ8 = kMode >= kE4m3Bf16;
   static constexpr int kRowBytes = kQ8 ? kDD : 2 * kDD;
   static constexpr int kTileB = kPiece * kRowBytes;            // one of K, V
-  static constexpr int kStageB = 2 * kTileB + (kQ8 ? 128 : 0); // + 16 K scales, 16 V scales
+  static constexpr int kStageB = 2 * kTileB + (kQ8 ? 128 : 0); // + 16 (K scale, V scale)
   static constexpr int kStages = kQ8 ? 4 : 3;
   // CTAs an SM, against copies in flight per warp (227 KB, 65536 registers):
   // 64 e4m3 sequences of up to 8192 keys took 159 us with 3 CTAs of 4 stages,
@@ -82,10 +82,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ float lds32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void lds64(uint32_t addr, float& a, float& b) {
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(addr) : "memory");
 }
 template <bool kHalf>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -229,10 +227,12 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
           const uint32_t st = ring + put * R::kStageB;
           const uint8_t* ks = kb + (pg * c.sk[0] + off * c.sk[1]) * kEl;
           const uint8_t* vs = vb + (pg * c.sv[0] + off * c.sv[1]) * kEl;
+          // (whole: some row sees every key of the piece, so all of it is copied)
+          const bool whole = j0 + kPiece - 1 <= any_hi && (j0 >= any_lo || j0 + kPiece <= firsts);
 #pragma unroll
           for (int i = 0; i < kPiece / kRowsAt; ++i) {
             const int r = cr + i * kRowsAt, j = j0 + r;
-            const bool take = j <= any_hi && (j >= any_lo || j < firsts);
+            const bool take = whole || (j <= any_hi && (j >= any_lo || j < firsts));
             // 16-bit rows: the 16-byte chunk index is permuted by the row so
             // that ldmatrix reads eight rows without bank conflicts; e4m3
             // rows by bit 2 of the index and the row's low bit, for the
@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
           }
           if constexpr (kQ8) {
             const int j = j0 + (lane & 15);
-            cp4(st + 2 * R::kTileB + lane * 4, scb + pg * scp + off * scr, j <= any_hi && (j >= any_lo || j < firsts));
+            cp4(st + 2 * R::kTileB + (lane & 15) * 8 + (lane >> 4) * 4, scb + pg * scp + off * scr,
+                whole || (j <= any_hi && (j >= any_lo || j < firsts)));
           }
         }
       }
@@ -375,8 +376,7 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
         if constexpr (kQ8) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            ksc[i] = lds32(st + 2 * R::kTileB + (g8 + 8 * i) * 4);
-            vsc[i] = lds32(st + 2 * R::kTileB + 64 + (g8 + 8 * i) * 4);
+            lds64(st + 2 * R::kTileB + (g8 + 8 * i) * 8, ksc[i], vsc[i]);
             lv[i] = fminf(fmaxf(__log2f(fabsf(vsc[i])), -60.f), 120.f);
           }
         }
