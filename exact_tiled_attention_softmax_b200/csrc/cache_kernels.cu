@@ -40,6 +40,13 @@ __device__ __forceinline__ float row_scale(float a) {
   const float s = __fdiv_rn(a, kE4m3Max);
   return s == 0.f ? 1.f : s;
 }
+// The same for a in [2^-80, 2^96]; usual: false outside (and for a NaN).
+__device__ __forceinline__ float row_scale_usual(float a, bool& usual) {
+  constexpr float r = 1.f / kE4m3Max;
+  usual = a >= 0x1p-80f && a <= 0x1p96f;
+  const float q = a * r;
+  return fmaf(fmaf(-q, kE4m3Max, a), r, q);
+}
 
 // max that keeps a NaN (fmaxf drops it).
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -48,20 +55,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// x / s correctly rounded, from the correctly rounded reciprocal r of s: the
-// quotient estimate's exact remainder, times r, corrects it (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990). The remainder is exact while nothing leaves the normal range;
-// callers take it for scales in [2^-90, 2^90], where a quotient that could
-// still round to a nonzero code (at least 2^-11) has a normal remainder.
-// Two quotients in packed fp32.
+// Quotients and reciprocals without branches, by the remainder corrections of
+// Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor" (1990): 1/s from an estimate r as r + r (1 - r s), and x / s from
+// q = x r as q + r (x - q s), each residual exact in one fma. Correctly rounded
+// while nothing leaves the normal range; callers take them for scales in
+// [2^-90, 2^90], where a quotient that could still round to a nonzero code
+// (at least 2^-11) has a normal remainder.
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return fmaf(r, fmaf(-r, s, 1.f), r);
+}
+// Two quotients in packed fp32. (The correction loses the sign of -0: it is put
+// back.)
 __device__ __forceinline__ void quotients(float& x0, float& x1, float s, float r) {
+  const float s0 = x0, s1 = x1;
   asm("{\n\t.reg .b64 x, q, d, ns, rr;\n\t"
       "mov.b64 x, {%0, %1};\n\tmov.b64 ns, {%2, %2};\n\tmov.b64 rr, {%3, %3};\n\t"
       "mul.rn.f32x2 q, x, rr;\n\tfma.rn.f32x2 d, q, ns, x;\n\tfma.rn.f32x2 q, d, rr, q;\n\t"
       "mov.b64 {%0, %1}, q;\n\t}"
       : "+f"(x0), "+f"(x1)
       : "f"(-s), "f"(r));
+  x0 = copysignf(x0, s0);
+  x1 = copysignf(x1, s1);
 }
 
 template <typename T>
@@ -172,7 +189,7 @@ cache_write_vec(CacheP c, const TS* k, int64_t snk0, int64_t snk1, const TS* v, 
   const int lane = threadIdx.x & 31, hl = lane & 15;
   const bool isv = lane >= 16;
   const int width = isv ? c.dv : c.d;
-  const TS* src = (isv ? v + (int64_t)t * snv0 : k + (int64_t)t * snk0);
+  const TS* src = (isv ? v : k) + (int64_t)t * (isv ? snv0 : snk0);
   const int64_t sh = isv ? snv1 : snk1;
   Vec8<TS> x[kHeadBlock][kCh];
 #pragma unroll
@@ -182,14 +199,24 @@ cache_write_vec(CacheP c, const TS* k, int64_t snk0, int64_t snk1, const TS* v, 
       if (h0 + e < c.Hkv && ch * 128 + hl * 8 < width) x[e][ch].load(src + (h0 + e) * sh + ch * 128 + hl * 8);
   int64_t pg, off;
   if (!slot_of(c, t, pg, off)) return;
-  const int64_t* sc = isv ? c.sv : c.sk;
-  const int64_t base = pg * sc[0] + off * sc[1];
+  // (strides as selected values: a selected pointer into the parameters would
+  // make every use an indexed constant load)
+  const int64_t sp = isv ? c.sv[0] : c.sk[0], so = isv ? c.sv[1] : c.sk[1], sc = isv ? c.sv[2] : c.sk[2];
+  uint8_t* pool = const_cast<uint8_t*>(static_cast<const uint8_t*>(isv ? c.v : c.k));
+  const int64_t base = pg * sp + off * so + (int64_t)h0 * sc;
+  [[maybe_unused]] float* scale_at = nullptr;
+  [[maybe_unused]] int64_t scale_step = 0;
+  if constexpr (kQuant) {
+    scale_step = isv ? c.svs[2] : c.sks[2];
+    scale_at = const_cast<float*>(isv ? c.vs : c.ks) + pg * (isv ? c.svs[0] : c.sks[0]) +
+               off * (isv ? c.svs[1] : c.sks[1]) + (int64_t)h0 * scale_step;
+  }
 #pragma unroll
   for (int e = 0; e < kHeadBlock; ++e) {
     if (h0 + e >= c.Hkv) break;
-    const int64_t row = base + (int64_t)(h0 + e) * sc[2];
+    const int64_t row = base + e * sc;
     if constexpr (!kQuant) {
-      TS* dst = const_cast<TS*>(static_cast<const TS*>(isv ? c.v : c.k)) + row;
+      TS* dst = reinterpret_cast<TS*>(pool) + row;
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch)
         if (ch * 128 + hl * 8 < width) x[e][ch].store(dst + ch * 128 + hl * 8);
@@ -200,10 +227,11 @@ cache_write_vec(CacheP c, const TS* k, int64_t snk0, int64_t snk1, const TS* v, 
         if (ch * 128 + hl * 8 < width) a = max_nan(a, x[e][ch].top());
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));  // within the half-warp
-      const float s = row_scale(a);
-      uint8_t* dst = const_cast<uint8_t*>(static_cast<const uint8_t*>(isv ? c.v : c.k)) + row;
-      const bool usual = s >= 0x1p-90f && s <= 0x1p90f;  // false for a NaN too
-      const float rs = __frcp_rn(s);
+      bool usual;
+      float s = row_scale_usual(a, usual);
+      if (!usual) s = row_scale(a);
+      const float rs = reciprocal(s);
+      uint8_t* dst = pool + row;
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch)
         if (ch * 128 + hl * 8 < width) {
@@ -218,10 +246,10 @@ cache_write_vec(CacheP c, const TS* k, int64_t snk0, int64_t snk1, const TS* v, 
               // one division in the code, for the element that i selects
               float g = f[0];
 #pragma unroll
-              for (int a = 1; a < 8; ++a) g = i == a ? f[a] : g;
+              for (int b = 1; b < 8; ++b) g = i == b ? f[b] : g;
               g = __fdiv_rn(g, s);
 #pragma unroll
-              for (int a = 0; a < 8; ++a) f[a] = i == a ? g : f[a];
+              for (int b = 0; b < 8; ++b) f[b] = i == b ? g : f[b];
             }
           }
           uint32_t w[2];
@@ -230,10 +258,7 @@ cache_write_vec(CacheP c, const TS* k, int64_t snk0, int64_t snk1, const TS* v, 
             w[i] = (uint32_t)e4m3x2(f[4 * i], f[4 * i + 1]) | ((uint32_t)e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16);
           *reinterpret_cast<uint2*>(dst + ch * 128 + hl * 8) = make_uint2(w[0], w[1]);
         }
-      if (hl == 0) {
-        const int64_t* ss = isv ? c.svs : c.sks;
-        const_cast<float*>(isv ? c.vs : c.ks)[pg * ss[0] + off * ss[1] + (int64_t)(h0 + e) * ss[2]] = s;
-      }
+      if (hl == 0) scale_at[e * scale_step] = s;
     }
   }
 }

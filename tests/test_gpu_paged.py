@@ -105,6 +105,27 @@ def test_write_of_special_rows():
         assert ((got[5] - k[5, 0].cpu()).abs() <= k[5, 0].cpu().abs() * 2.0 ** -4 + 2.0 ** -10).all()
 
 
+@pytest.mark.parametrize("src", ["bf16", "f16", "f32"])
+def test_codes_at_every_magnitude(src):
+    """Codes and scales equal the correctly rounded quotients, bit for bit, for
+    rows of every magnitude the type holds, values on borders among them."""
+    g = torch.Generator().manual_seed(4)
+    top = {"bf16": 127, "f16": 15, "f32": 127}[src]
+    n = 2 * top + 10
+    mag = 2.0 ** torch.linspace(-top - 8, top - 1, n).double()
+    x = torch.randn(n, 2, 128, generator=g).double().clamp(-1, 1)
+    x[:, 0, :64] = torch.randint(-448, 449, (n, 64), generator=g) / 448.0  # on and between codes
+    x = (x * mag[:, None, None]).to(DT[src])
+    cache, _, _ = make_cache([n], 16, 2, 128, 128, E4M3, seed=1)
+    eta.attn_cache_write(x.cuda(), x.flip(0).contiguous().cuda(), cache)
+    pos = torch.arange(n)
+    at = cache.block_table[0].long().cpu()[pos // 16], pos % 16
+    for pool, scale, rows in ((cache.k, cache.k_scale, x), (cache.v, cache.v_scale, x.flip(0))):
+        code, s = quantise(rows)
+        assert torch.equal(bits(scale)[at], s.view(torch.int32))
+        assert torch.equal(pool.view(torch.uint8).cpu()[at], code.view(torch.uint8))
+
+
 def test_write_and_read_report_bad_pages_and_lengths():
     ws = torch.empty(256, dtype=torch.uint8, device="cuda")
     cache, K, _ = make_cache([40, 20], 16, 2, 128, 128, torch.bfloat16, seed=2)
