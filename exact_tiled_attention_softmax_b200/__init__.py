@@ -173,7 +173,7 @@ def _tensor(t: torch.Tensor | None):
 
 
 def _ref(c):
-    return ctypes.byref(c) if c is not None else None
+    return c  # ctypes passes a structure to a pointer argument by reference
 
 
 def _check_on(device: torch.device, *tensors) -> None:
@@ -182,8 +182,9 @@ def _check_on(device: torch.device, *tensors) -> None:
     pointer, or another GPU's, from its own."""
     if device.type != "cuda":
         raise ValueError(f"attention tensors must be CUDA tensors (got {device})")
+    index = device.index
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"a tensor is on {t.device}, the query on {device}")
 
 
@@ -314,7 +315,7 @@ def _stream_handle(stream) -> int:
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
     # 256-byte aligned: the caching allocator hands out 512-byte aligned blocks.
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def _is_topk(allowed: AllowedSet | None) -> bool:
@@ -343,9 +344,9 @@ def attn_fwd(q, k, v, allowed: AllowedSet | None = None, scale: float | None = N
     if scale is None:
         scale = q.shape[-1] ** -0.5
     if out is None:
-        out = torch.empty(*q.shape[:-1], v.shape[-1], dtype=q.dtype, device=q.device)
+        out = q.new_empty((*q.shape[:-1], v.shape[-1]))
     if lse is None:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
     m = allowed.to_c() if allowed else None
     cq, ck, cv, co, cl = (_tensor(x) for x in (q, k, v, out, lse))
     need = lib.attn_fwd_workspace_size(_ref(cq), _ref(ck), _ref(cv), _ref(m))

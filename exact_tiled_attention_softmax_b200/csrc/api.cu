@@ -186,6 +186,8 @@ size_t bwd_topk_bytes(const Topk& s, const attn_tensor* q, const attn_mask* m) {
 
 int elem_bytes(int32_t dt) { return dt == ATTN_F32 ? 4 : dt == ATTN_E4M3 ? 1 : 2; }
 
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 // A tensor the caller hands over as [shape...] of dtype dt: ranks, strides
 // that do not alias elements, element alignment, a pointer when not empty.
 attn_status check_pool(const attn_tensor* t, int ndim, const int64_t* shape, bool inner) {
@@ -196,7 +198,7 @@ attn_status check_pool(const attn_tensor* t, int ndim, const int64_t* shape, boo
     if (shape[i] > 1 && t->stride[i] < 1) return ATTN_ERR_INVALID_ARG;
   }
   if (n && !t->data) return ATTN_ERR_INVALID_ARG;
-  return reinterpret_cast<uintptr_t>(t->data) % elem_bytes(t->dtype) ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+  return aligned_to(t->data, elem_bytes(t->dtype)) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
 // Positions, windows and new tokens stay below 2^30, so that the kernels' 32-bit
@@ -231,7 +233,8 @@ attn_status check_cache(const attn_cache* c, CacheP& p) {
   }
   if (c->batch < 0 || c->max_pages < 0 || (c->batch > 1 && c->table_stride < c->max_pages)) return ATTN_ERR_INVALID_ARG;
   if (c->batch && (!c->seq_lens || (c->max_pages && !c->block_table))) return ATTN_ERR_INVALID_ARG;
-  if ((int64_t)c->max_pages * p.page_size > kMaxPositions) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned_to(c->seq_lens, 4) || !aligned_to(c->block_table, 4)) return ATTN_ERR_INVALID_ARG;
+  if ((int64_t)c->max_pages * p.page_size > kMaxPositions || c->batch > kMaxPositions) return ATTN_ERR_UNSUPPORTED;
   p.k = c->k.data;
   p.v = c->v.data;
   for (int i = 0; i < 3; ++i) {
@@ -251,7 +254,7 @@ attn_status check_cache(const attn_cache* c, CacheP& p) {
 
 // Rows of new tokens: every sequence's share must be whole when cu_q is NULL.
 attn_status check_rows(int64_t rows, const int32_t* cu_q, CacheP& p) {
-  if (!cu_q && (p.batch ? rows % p.batch : rows) != 0) return ATTN_ERR_INVALID_ARG;
+  if ((!cu_q && (p.batch ? rows % p.batch : rows) != 0) || !aligned_to(cu_q, 4)) return ATTN_ERR_INVALID_ARG;
   if (rows > kMaxPositions) return ATTN_ERR_UNSUPPORTED;
   p.cu_q = cu_q;
   p.rows = (int32_t)rows;
@@ -568,8 +571,7 @@ attn_status attn_bwd(const attn_tensor* q, const attn_tensor* k, const attn_tens
     if (t->dtype != q->dtype || !inner_contiguous(t)) return ATTN_ERR_INVALID_ARG;
   const size_t need = attn_bwd_workspace_size(q, k, v, mask);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != ATTN_OK) return st;
-  if (cudaMemsetAsync(status, 0, kStatusBytes, cs) != cudaSuccess) return ATTN_ERR_CUDA;
-  if ((int64_t)s.B * s.Hq * s.Tq == 0) return ATTN_OK;
+  const bool none = (int64_t)s.B * s.Hq * s.Tq == 0;
   float* delta = reinterpret_cast<float*>(ws + kStatusBytes);
   const size_t rows = (size_t)s.B * s.Hq * s.Tq;
   float* dq_acc = reinterpret_cast<float*>(ws + kStatusBytes + align_up(rows * sizeof(float), 256));
@@ -603,6 +605,11 @@ attn_status attn_bwd(const attn_tensor* q, const attn_tensor* k, const attn_tens
   const int64_t sdv[3] = {dv->stride[0], dv->stride[1], dv->stride[2]};
   const float* lsep = static_cast<const float*>(lse->data);
   cudaError_t e;
+  // The tensor-core path's first kernel clears the status word itself.
+  const bool tensor_cores =
+      !none && sm100_dense_supported(p, q, k, v, o) && sm100_dense_bwd_supported(p, do_, dq, dk, dv);
+  if (!tensor_cores && cudaMemsetAsync(status, 0, kStatusBytes, cs) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (none) return ATTN_OK;
   if (p.m.lse_fmt) {  // the reverse kernels read the natural-log, sink-inclusive LSE
     float* conv = reinterpret_cast<float*>(ws + need - lse_copy_bytes(mask, rows));
     if ((e = launch_lse_to_total(lsep, s.B, s.Hq, s.Tq, sl, 1, mask->sink, p.m.lse_fmt, conv, cs)) != cudaSuccess)
@@ -612,7 +619,7 @@ attn_status attn_bwd(const attn_tensor* q, const attn_tensor* k, const attn_tens
     sl[1] = s.Tq;
     sl[2] = 1;
   }
-  if (sm100_dense_supported(p, q, k, v, o) && sm100_dense_bwd_supported(p, do_, dq, dk, dv)) {
+  if (tensor_cores) {
     // With first keys the sink gradient sums an fp32 delta; without, the
     // product with the stored 16-bit O, whose rounding leaves it off by about
     // 1e-3 of the terms' size.
@@ -646,7 +653,8 @@ attn_status attn_cache_write(const attn_tensor* k, const attn_tensor* v, const i
   const int64_t ks[3] = {rows, p.Hkv, p.d}, vs[3] = {rows, p.Hkv, p.dv};
   if (!same_shape(k, 3, ks) || !same_shape(v, 3, vs) || !inner_contiguous(k) || !inner_contiguous(v))
     return ATTN_ERR_INVALID_ARG;
-  if (rows && (!k->data || !v->data)) return ATTN_ERR_INVALID_ARG;
+  const int el = elem_bytes(k->dtype);
+  if ((rows && (!k->data || !v->data)) || !aligned_to(k->data, el) || !aligned_to(v->data, el)) return ATTN_ERR_INVALID_ARG;
   if ((st = check_rows(rows, cu_q, p)) != ATTN_OK) return st;
   if (rows * p.Hkv >= kMaxRowWarps) return ATTN_ERR_UNSUPPORTED;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -700,7 +708,7 @@ attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn
   const int64_t rows = q->shape[0], Hq = q->shape[1];
   const int64_t qs[3] = {rows, Hq, p.c.d}, os[3] = {rows, Hq, p.c.dv}, ls[2] = {rows, Hq};
   if (!same_shape(q, 3, qs) || !inner_contiguous(q) || Hq < 1 || Hq % p.c.Hkv != 0) return ATTN_ERR_INVALID_ARG;
-  if (rows && !q->data) return ATTN_ERR_INVALID_ARG;
+  if ((rows && !q->data) || !aligned_to(q->data, elem_bytes(q->dtype))) return ATTN_ERR_INVALID_ARG;
   if ((st = check_pool(o, 3, os, true)) != ATTN_OK || (st = check_pool(lse, 2, ls, false)) != ATTN_OK) return st;
   if ((st = check_rows(rows, cu_q, p.c)) != ATTN_OK) return st;
   if (rows * Hq >= kMaxRowWarps) return ATTN_ERR_UNSUPPORTED;

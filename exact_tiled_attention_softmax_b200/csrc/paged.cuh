@@ -1,6 +1,6 @@
 // Paged K/V caches: the parameter block that every paged kernel takes, the
 // checked view of one sequence, and the launchers (internal; the C entry
-// points are in paged_api.cu).
+// points are in api.cu).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -37,7 +37,7 @@ struct PagedP {
   int64_t sl[2];
   int32_t Hq;
   int32_t dtype;  // attn_dtype of q and o
-  uint32_t flags; // ATTN_MASK_CAUSAL | WINDOW
+  uint32_t flags; // ATTN_MASK_CAUSAL | WINDOW | FIRST
   int64_t window, first;
   const float* sink;
   uint32_t lse_fmt;

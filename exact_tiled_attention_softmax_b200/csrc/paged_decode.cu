@@ -17,8 +17,8 @@
 // keys are cut into 64-key tiles (one 16-key piece per warp) and all tiles of
 // all items, in order, are dealt to the CTAs in equal consecutive shares, so
 // the load is even whatever the lengths are and the grid needs no length from
-// the host. An item that several CTAs share is joined by the last of them to
-// finish, in the CTAs' order, so the result does not depend on timing.
+// the host. decode_join_kernel adds the sums of an item that several CTAs share
+// in the CTAs' order, so the result does not depend on timing.
 #include <math.h>
 
 #include "paged.cuh"

@@ -1800,7 +1800,9 @@ template <bool kH>
 __global__ void __launch_bounds__(256)
 bwd_prepare_kernel(const uint16_t* o, int64_t so0, int64_t so1, int64_t so2, const uint16_t* g,
                    int64_t sg0, int64_t sg1, int64_t sg2, const float* lse, int64_t sl0, int64_t sl1, int64_t sl2,
-                   int B, int Hq, int T, int Tpad, float* lse2, float* dpad, float* delta, float* dq_acc) {
+                   int B, int Hq, int T, int Tpad, float* lse2, float* dpad, float* delta, float* dq_acc,
+                   uint32_t* status) {
+  if (blockIdx.x == 0 && threadIdx.x < kStatusBytes / 4) status[threadIdx.x] = 0u;  // later kernels set its bits
   const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31, hl = lane & 15;
   const int64_t nrows = (int64_t)B * Hq * Tpad;
@@ -2113,7 +2115,8 @@ cudaError_t sm100_dense_bwd(const DenseP& p, const void* o, const int64_t so[3],
   const int64_t rows = (int64_t)p.B * p.Hq * Tpad;  // a multiple of 128: eight rows per warp
   (f16 ? bwd_prepare_kernel<true> : bwd_prepare_kernel<false>)<<<(unsigned)((rows * 4 + 255) / 256), 256, 0, st>>>(
       static_cast<const uint16_t*>(o), so[0], so[1], so[2], static_cast<const uint16_t*>(g), sg[0], sg[1], sg[2], lse,
-      sl[0], sl[1], sl[2], p.B, p.Hq, p.Tq, Tpad, lse2, dpad, delta, det ? nullptr : dq_acc);
+      sl[0], sl[1], sl[2], p.B, p.Hq, p.Tq, Tpad, lse2, dpad, delta, det ? nullptr : dq_acc,
+      status);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   CUtensorMap mq, mk, mv, mg, mdq;
   if (!make_dq_map(&mdq, dq_acc, p.Tq, p.B * p.Hq) ||

@@ -13,7 +13,7 @@
 // sequence's end or in a page outside the pool take page 0, whose keys are
 // masked). An e4m3 tile lands in a raw buffer, and four warps turn it into the
 // 16-bit operand tiles: K's codes exactly (their scale multiplies the score
-// in fp32), V's times their scales, in fp16.
+// in fp32), V's times their scales over a power of two per 32 keys, in fp16.
 //
 // A masked key's V row may hold anything, and 0 times an infinity is not 0.
 // In tiles that some row sees only in part, or that hold such a box, the
@@ -24,8 +24,9 @@
 // Work split: plan_kernel lists the blocks of every sequence, deals whole items
 // (block, K/V head) to the CTAs round by round, so that the CTAs walk the same
 // head's tiles in step and find them in L2, and cuts the tiles of the
-// remaining items into shares that even the CTAs out. An item in several
-// shares is joined by the CTA that finishes last, in share order.
+// remaining items into shares that even the CTAs out. A share of an item
+// leaves its sums in the workspace, and chunk_join_kernel adds an item's shares
+// in the CTAs' order, so the result does not depend on timing.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>

@@ -300,8 +300,10 @@ attn_status attn_bwd_noalloc(const attn_tensor* q, const attn_tensor* k,
  * and not read back (ATTN_DEVERR_PAGE); seq_lens and cu_q are clamped to
  * [0, max_pages * page_size] and [0, rows], and new tokens at negative
  * positions (n_b > seq_lens[b]) are not written and see no key
- * (ATTN_DEVERR_RAGGED for all of these). Rows of q, k, v, o and lse that
- * belong to no sequence (past cu_q[batch]) are neither read nor written. */
+ * (ATTN_DEVERR_RAGGED for all of these). Rows of q, k and v that belong to no
+ * sequence (past cu_q[batch]) have no influence, and those of o and lse are
+ * left as they were. Data, table, length and cu_q pointers are aligned to
+ * their elements. */
 typedef struct attn_cache {
   attn_tensor k, v;
   attn_tensor k_scale, v_scale;
@@ -346,8 +348,9 @@ size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, 
  * of the other three; o's is q's. Scores take the cached code times its
  * scale exactly (the scale multiplies the fp32 score). The tensor-core kernels
  * round the probabilities to the cache's 16-bit type, to fp16 for an
- * ATTN_E4M3 cache, times the value row's scale where max_q asks for the
- * few-token kernel; the other one takes value rows as fp16(code * scale).
+ * ATTN_E4M3 cache: times the value row's scale where max_q asks for the
+ * few-token kernel; the other one takes value rows as fp16(code * scale / 2^e)
+ * with one power of two per 32 keys, which multiplies their probabilities.
  * Infinities and NaN in rows a query does not see
  * do not reach it. A row whose allowed scores are all -inf counts as empty.
  * max_q: the largest n_b, if the caller knows it, else 0: it chooses

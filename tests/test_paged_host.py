@@ -201,3 +201,25 @@ def test_quartic_exponential():
     got = (p.view(np.int32) + (n << 23)).view(np.float32).astype(np.float64)
     # the fit's error, and four roundings of 2^-24 (one is relative to terms below 1)
     assert np.abs(got / np.exp2(x.astype(np.float64)) - 1).max() < 3.1e-6 + 4 * 2.0 ** -23
+
+
+def test_addresses_between_elements_are_refused(lib):  # noqa: F811
+    bad = eta.ATTN_ERR_INVALID_ARG
+    odd = _t([6, 2, 128], data=0x1001)
+    assert _write(lib, _cache(), odd) == bad
+    assert _write(lib, _cache(), v=odd) == bad
+    half = _t([6, 2, 128], 0, data=0x1002)  # fp32 rows at a 2-byte boundary
+    assert _write(lib, _cache(3), half, _t([6, 2, 128], 0)) == bad
+    assert _fwd(lib, _cache(), _t([6, 4, 128], data=0x1001)) == bad
+    for field in ("block_table", "seq_lens"):
+        c = _cache()
+        setattr(c, field, 0x5002)
+        assert _write(lib, c) == bad and _fwd(lib, c) == bad and _read(lib, c) == bad
+    assert _write(lib, _cache(), cu=0x7001) == bad
+    assert _fwd(lib, _cache(), cu=0x7001) == bad
+
+
+def test_more_sequences_than_positions_are_refused(lib):  # noqa: F811
+    c = _cache(batch=(1 << 30) + 1)
+    assert _write(lib, c) == eta.ATTN_ERR_UNSUPPORTED
+    assert _fwd(lib, c) == eta.ATTN_ERR_UNSUPPORTED
