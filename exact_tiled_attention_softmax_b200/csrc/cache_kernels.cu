@@ -174,7 +174,7 @@ struct Vec8<__half> : Vec8of16<__half2, __half> {
 __device__ __forceinline__ bool slot_of(const CacheP& c, int t, int64_t& pg, int64_t& off) {
   const int b = warp_seq_of(c, t);
   if (b < 0) return false;
-  const SeqView s = seq_view(c, b);
+  const SeqView s = warp_seq_view(c, b);
   const int pos = (int)s.L - s.n + (t - s.q0);
   if (pos < 0 || pos >= (int)s.L) return false;
   pg = page_of(c, b, pos);

@@ -72,6 +72,16 @@ __device__ __forceinline__ SeqView seq_view(const CacheP& c, int b) {
   return s;
 }
 
+// The same for a whole (converged) warp: one reading, so that its lanes agree even
+// while someone else writes the arrays.
+__device__ __forceinline__ SeqView warp_seq_view(const CacheP& c, int b) {
+  SeqView s = seq_view(c, b);
+  s.q0 = __shfl_sync(0xffffffffu, s.q0, 0);
+  s.n = __shfl_sync(0xffffffffu, s.n, 0);
+  s.L = __shfl_sync(0xffffffffu, (int)s.L, 0);  // below 2^30
+  return s;
+}
+
 // Reports cu_q and seq_lens entries that seq_view clamps, or whose new tokens
 // do not fit their sequence. For one block of a launch, all threads.
 __device__ __forceinline__ void report_ragged(const CacheP& c, uint32_t* status) {
@@ -95,13 +105,13 @@ __device__ __forceinline__ int warp_seq_of(const CacheP& c, int t) {
     return t / each < c.batch ? t / each : -1;
   }
   const int lane = threadIdx.x & 31;
-  int b = 0;
+  int b = 0;  // (the same in every lane: it counts ballots)
   for (int b0 = 0; b0 < c.batch; b0 += 32) {
     const bool ends = b0 + lane < c.batch && c.cu_q[b0 + lane + 1] <= t;
     b += __popc(__ballot_sync(0xffffffffu, ends));
   }
   if (b >= c.batch) return -1;
-  return c.cu_q[b] <= t && t < c.cu_q[b + 1] ? b : -1;
+  return __all_sync(0xffffffffu, c.cu_q[b] <= t && t < c.cu_q[b + 1]) ? b : -1;
 }
 
 // The page that holds position pos (below 2^30) of sequence b, or -1 when the table names

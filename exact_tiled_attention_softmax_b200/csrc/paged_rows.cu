@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_rows_kernel(PagedP p) {
   const int t = (int)(warp / p.Hq), h = (int)(warp % p.Hq);
   const int b = warp_seq_of(c, t);
   if (b < 0) return;
-  const SeqView s = seq_view(c, b);
+  const SeqView s = warp_seq_view(c, b);
   const int64_t pos = s.L - s.n + (t - s.q0);  // the query's key position
   const int kvh = h / (p.Hq / c.Hkv);
   const TQ* q = static_cast<const TQ*>(p.q) + t * p.sq[0] + h * p.sq[1];

@@ -3,7 +3,9 @@
 // tiles of all items, in order, are dealt to the CTAs of one wave in equal
 // consecutive shares. Lengths are read on the device, so a captured call
 // serves whatever lengths it meets, and every SM gets the same number of tiles
-// whether the batch holds one long sequence or many ragged ones. An item
+// whether the batch holds one long sequence or many ragged ones. (The lengths
+// must not change meanwhile; if they do, the readings disagree and the results
+// mean nothing, but every index stays within its range.) An item
 // whose tiles fall to several CTAs leaves one partial result (running maximum,
 // sum and unnormalised rows, fp32) per CTA in the workspace, and the CTA that
 // begins it a record of what is to be joined; a second, small kernel joins
@@ -62,14 +64,14 @@ struct Item {
   __device__ __forceinline__ int tile_at(int k) const { return k < nf ? k : k - nf + (lo > nf ? lo : nf); }
 };
 
-// The key tiles that some new token of sequence b sees, and its row blocks.
-// One tile at least, so that a sequence without keys still gets its rows
-// written.
+// The key tiles that some new token of sequence b (whose view s is) sees, and
+// its row blocks. One tile at least, so that a sequence without keys still gets
+// its rows written.
 template <int kTile, int kRows>
-__device__ __forceinline__ Item seq_tiles(const PagedP& p, int b) {
+__device__ __forceinline__ Item seq_tiles(const PagedP& p, int b, const SeqView& s) {
   Item it;
   it.b = b;
-  it.s = seq_view(p.c, b);
+  it.s = s;
   const int64_t L = it.s.L;
   it.hi = (int)((L + kTile - 1) / kTile);
   it.lo = it.nf = 0;
@@ -112,7 +114,7 @@ __device__ __forceinline__ Share split_share(const PagedP& p, const SplitP& sp, 
   const int B = p.c.batch;
   auto units = [&](int b) {
     if (b >= B) return (int64_t)0;
-    const Item it = seq_tiles<kTile, kRows>(p, b);
+    const Item it = seq_tiles<kTile, kRows>(p, b, seq_view(p.c, b));
     return (int64_t)it.tiles * it.blocks * p.c.Hkv;
   };
   int64_t before, total = 0, mine = 0;
@@ -134,6 +136,11 @@ __device__ __forceinline__ Share split_share(const PagedP& p, const SplitP& sp, 
   sh.u = me * total / ctas;
   sh.left = (me + 1) * total / ctas - sh.u;
   int64_t base = 0;
+  if (threadIdx.x == 0) {
+    ss.b = 0;
+    ss.rem = 0;
+  }
+  __syncthreads();
   for (int b0 = 0; b0 < B; b0 += blockDim.x) {
     if (B > blockDim.x) {
       mine = units(b0 + threadIdx.x);
@@ -148,16 +155,19 @@ __device__ __forceinline__ Share split_share(const PagedP& p, const SplitP& sp, 
   }
   __syncthreads();
   sh.b = ss.b;
-  const int tiles = seq_tiles<kTile, kRows>(p, sh.b).tiles;
+  const int tiles = seq_tiles<kTile, kRows>(p, sh.b, warp_seq_view(p.c, sh.b)).tiles;
   sh.sub = (int)(ss.rem / tiles);
   sh.at = ss.rem % tiles;
   return sh;
 }
 
 template <int kTile, int kRows>
-__device__ __forceinline__ Item split_item(const PagedP& p, const Share& sh) {
-  Item it = seq_tiles<kTile, kRows>(p, sh.b);
+__device__ __forceinline__ Item split_item(const PagedP& p, Share& sh) {
+  Item it = seq_tiles<kTile, kRows>(p, sh.b, warp_seq_view(p.c, sh.b));
+  if (it.blocks < 1) it.blocks = 1;  // (only with lengths that change)
+  if (sh.at >= it.tiles) sh.at = it.tiles - 1;
   it.h = sh.sub / it.blocks;  // the row blocks of a head follow one another: its keys are in L2 by then
+  if (it.h >= p.c.Hkv) it.h = p.c.Hkv - 1;
   it.row0 = (sh.sub % it.blocks) * kRows;
   const int all = it.s.n * (p.Hq / p.c.Hkv);
   it.rows = all - it.row0 < kRows ? all - it.row0 : kRows;
@@ -175,12 +185,14 @@ __device__ __forceinline__ void split_advance(const PagedP& p, Share& sh, const 
   sh.sub = 0;
   if (sh.left > 0) {  // then a later sequence has rows
     do ++sh.b;
-    while (seq_view(p.c, sh.b).n == 0);
+    while (sh.b < p.c.batch && warp_seq_view(p.c, sh.b).n == 0);
+    if (sh.b >= p.c.batch) sh.left = 0;
   }
 }
 
 __device__ __forceinline__ int split_owner(const Share& sh, int64_t u) {
-  return (int)(((u + 1) * sh.ctas - 1) / sh.total);
+  const int64_t o = ((u + 1) * sh.ctas - 1) / sh.total;
+  return o < sh.ctas ? (int)o : sh.ctas - 1;
 }
 
 // One row's finish: the factor that turns the unnormalised row into the
