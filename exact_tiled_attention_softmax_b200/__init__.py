@@ -113,15 +113,15 @@ def load_library():
     lib.attn_bwd.argtypes = [T, T, T, T, T, T, M, ctypes.c_float, T, T, T, vp, vp, sz, vp]
     lib.attn_bwd_noalloc.restype = ctypes.c_int
     lib.attn_bwd_noalloc.argtypes = [T, T, T, T, T, T, M, ctypes.c_float, T, T, T, vp, vp]
-    C = ctypes.POINTER(AttnCacheC)
+    # Descriptors of the paged calls go as packed bytes (or by reference).
     lib.attn_cache_write.restype = ctypes.c_int
-    lib.attn_cache_write.argtypes = [T, T, vp, C, vp, sz, vp]
+    lib.attn_cache_write.argtypes = [vp, vp, vp, vp, vp, sz, vp]
     lib.attn_cache_read.restype = ctypes.c_int
-    lib.attn_cache_read.argtypes = [C, T, T, vp, sz, vp]
+    lib.attn_cache_read.argtypes = [vp, vp, vp, vp, sz, vp]
     lib.attn_paged_workspace_size.restype = sz
-    lib.attn_paged_workspace_size.argtypes = [T, C, M]
+    lib.attn_paged_workspace_size.argtypes = [vp, vp, M]
     lib.attn_paged_fwd.restype = ctypes.c_int
-    lib.attn_paged_fwd.argtypes = [T, vp, C, M, ctypes.c_float, ctypes.c_int32, T, T, vp, sz, vp]
+    lib.attn_paged_fwd.argtypes = [vp, vp, vp, M, ctypes.c_float, ctypes.c_int32, vp, vp, vp, sz, vp]
     lib.attn_get_status.restype = ctypes.c_int
     lib.attn_get_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.attn_selftest_wait_timeout.restype = ctypes.c_int
@@ -168,8 +168,12 @@ def _fields(t: torch.Tensor) -> tuple:
     return (t.data_ptr() if t.numel() else 0, _DTYPES.get(t.dtype, -1), n, *t.shape, *pad, *t.stride(), *pad)
 
 
+def _packed(t: torch.Tensor) -> bytes:
+    return _TENSOR.pack(*_fields(t))
+
+
 def _tensor(t: torch.Tensor | None):
-    return None if t is None else AttnTensorC.from_buffer_copy(_TENSOR.pack(*_fields(t)))
+    return None if t is None else AttnTensorC.from_buffer_copy(_packed(t))
 
 
 def _ref(c):
@@ -489,6 +493,10 @@ class PagedCache:
 
     def to_c(self) -> AttnCacheC:
         """The C descriptor, after the checks that raw pointers cannot carry."""
+        return AttnCacheC.from_buffer_copy(self.packed())
+
+    def packed(self) -> bytes:
+        """to_c's bytes."""
         table, lens = self.block_table, self.seq_lens
         _check_mask_tensor(table, "block_table", _INT32, _TWO_DIMS)
         _check_mask_tensor(lens, "seq_lens", _INT32, _ONE_DIM)
@@ -496,11 +504,11 @@ class PagedCache:
         if B != lens.shape[0]:
             raise ValueError("block_table and seq_lens hold different numbers of sequences")
         _check_on(self.k.device, self.v, table, lens, self.k_scale, self.v_scale)
-        return AttnCacheC.from_buffer_copy(_CACHE.pack(
+        return _CACHE.pack(
             *_fields(self.k), *_fields(self.v),
             *(_NO_TENSOR if self.k_scale is None else _fields(self.k_scale)),
             *(_NO_TENSOR if self.v_scale is None else _fields(self.v_scale)),
-            table.data_ptr(), table.stride(0), pages, B, lens.data_ptr()))
+            table.data_ptr(), table.stride(0), pages, B, lens.data_ptr())
 
 
 def _cu_q_ptr(cu_q, cache: PagedCache):
@@ -533,9 +541,9 @@ def attn_cache_write(k, v, cache: PagedCache, cu_q=None, *, workspace=None, stre
     each), quantised when the cache is e4m3. With a workspace of at least 256
     bytes, attn_get_status reports bad pages and lengths. Returns the cache."""
     device = cache.k.device
-    c, cu = cache.to_c(), _cu_q_ptr(cu_q, cache)
+    c, cu = cache.packed(), _cu_q_ptr(cu_q, cache)
     _check_on(device, k, v, workspace)
-    rc = _on_device(device, load_library().attn_cache_write, stream, _tensor(k), _tensor(v), cu, c,
+    rc = _on_device(device, load_library().attn_cache_write, stream, _packed(k), _packed(v), cu, c,
                     *_workspace_args(workspace))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_write")
@@ -562,9 +570,9 @@ def attn_cache_read(cache: PagedCache, max_len: int | None = None, *, dtype=None
         B = cache.seq_lens.shape[0]
         k = torch.zeros(B, H, T, d, dtype=dtype, device=device) if k is None else k
         v = torch.zeros(B, H, T, cache.v.shape[3], dtype=dtype, device=device) if v is None else v
-    c = cache.to_c()
+    c = cache.packed()
     _check_on(device, k, v, workspace)
-    rc = _on_device(device, load_library().attn_cache_read, stream, c, _tensor(k), _tensor(v),
+    rc = _on_device(device, load_library().attn_cache_read, stream, c, _packed(k), _packed(v),
                     *_workspace_args(workspace))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_read")
@@ -574,7 +582,7 @@ def attn_cache_read(cache: PagedCache, max_len: int | None = None, *, dtype=None
 def attn_paged_workspace_size(q, cache: PagedCache, allowed: AllowedSet | None = None) -> int:
     m = allowed.to_c() if allowed else None
     with torch.cuda.device(q.device):
-        return int(load_library().attn_paged_workspace_size(_tensor(q), cache.to_c(), m))
+        return int(load_library().attn_paged_workspace_size(_packed(q), cache.packed(), m))
 
 
 def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None = None, scale: float | None = None, *,
@@ -594,7 +602,7 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
     if lse is None:
         lse = q.new_empty((rows, heads), dtype=torch.float32)
     m = allowed.to_c() if allowed else None
-    cq, c, cu = _tensor(q), cache.to_c(), _cu_q_ptr(cu_q, cache)
+    cq, c, cu = _packed(q), cache.packed(), _cu_q_ptr(cu_q, cache)
     _check_on(device, cache.k, out, lse, workspace, *(allowed.tensors() if allowed else ()))
 
     def call(s):
@@ -606,7 +614,7 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
             else:  # from that stream's pool: freed here, reused there after the call
                 with torch.cuda.stream(stream):
                     ws = _workspace(need, device)
-        return lib.attn_paged_fwd(cq, cu, c, m, scale, int(max_q), _tensor(out), _tensor(lse), *_workspace_args(ws), s)
+        return lib.attn_paged_fwd(cq, cu, c, m, scale, int(max_q), _packed(out), _packed(lse), *_workspace_args(ws), s)
 
     rc = _on_device(device, call, stream)
     if rc != ATTN_OK:

@@ -1,6 +1,6 @@
-// Attention over a paged cache for few new tokens per sequence (at most 16
-// (token, head of the group) rows per K/V head): 16-bit or e4m3 cache, d = dv =
-// 128, pages of a multiple of 16 positions.
+// Attention over a paged cache for few new tokens per sequence (16 or 32 (token,
+// head of the group) rows per K/V head, paged_decode_supported): 16-bit or e4m3
+// cache, d = dv = 128, pages of a multiple of 16 positions.
 //
 // The arithmetic is 4 flops per cached element and row, so with up to 16 rows
 // the cache's bytes bound it, and what matters is to keep enough of them in
@@ -41,7 +41,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kDD = 128;          // head width
-constexpr int kMaxRows = 16;      // query rows per item: 8 or 16
+constexpr int kMaxRows = 16;      // most query rows per item: 8 or 16
 constexpr int kDWarps = 4;
 constexpr int kDThreads = kDWarps * 32;
 constexpr int kPiece = 16;        // keys per warp and tile
@@ -624,9 +624,15 @@ cudaError_t launch_mode(const PagedP& p, SplitP sp, cudaStream_t st) {
                       kJoinRows * 32, 0, st, p, sp);
 }
 
+// Blocks of 8 or 16 rows. A 16-bit cache is bound by its bytes either way (64
+// sequences of 8192 keys: 317 us with 8 rows and with 16); an e4m3 one by
+// instructions, 200 against 310 us, so that three blocks of 8 take less than two
+// of 16 (20 rows: 572 against 626 us) and two of 8 more than one of 16 (12 rows:
+// 386 against 323 us).
 template <int kMode>
 cudaError_t launch_rows(const PagedP& p, int rows, const SplitP& sp, cudaStream_t st) {
-  return rows <= 8 ? launch_mode<kMode, 1>(p, sp, st) : launch_mode<kMode, 2>(p, sp, st);
+  const bool eights = rows <= 8 || (kMode >= kE4m3Bf16 && rows > 16 && rows <= 24);
+  return eights ? launch_mode<kMode, 1>(p, sp, st) : launch_mode<kMode, 2>(p, sp, st);
 }
 
 constexpr int kMostCtas = 4;  // of any form, an SM
@@ -654,8 +660,17 @@ bool paged_pieces_ok(const PagedP& p) {
   return bits % 16 == 0;
 }
 
+// Where this kernel is taken and not the chunk kernel, measured with 32 heads
+// over 8 (this kernel / the chunk kernel, us). Up to 16 rows always: 64 sequences
+// of 8192 keys, 16 rows, bf16 334 / 566, e4m3 320 / 717. Up to 32 rows, where the
+// cache is read twice, for e4m3 (64 of 8192: 20 rows 572 / 691, 32 rows 679 / 709;
+// 16 of 2048: 57 / 67; one of 32768: 56 / 65), and for 16-bit caches where there
+// are fewer K/V heads than SMs to share out (16 of 2048: 49-52 / 53; one of 32768:
+// 54-56 / 57; one of 2048: 15 / 21), but not beyond (64 of 8192: 694 / 601). From
+// 48 rows on the chunk kernel (16 of 2048, e4m3: 75 / 68).
 bool paged_decode_supported(const PagedP& p, int32_t max_q) {
-  return paged_pieces_ok(p) && (int64_t)max_q * (p.Hq / p.c.Hkv) <= kMaxRows;
+  const bool twice = p.c.dtype == ATTN_E4M3 || (int64_t)p.c.batch * p.c.Hkv <= sm_count();
+  return paged_pieces_ok(p) && (int64_t)max_q * (p.Hq / p.c.Hkv) <= (twice ? 2 : 1) * kMaxRows;
 }
 
 size_t paged_decode_workspace_bytes() {

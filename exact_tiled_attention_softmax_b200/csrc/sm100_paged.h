@@ -9,8 +9,8 @@ int sm_count();  // of the current device
 // Widths, types, page size and alignment that the tensor-core paths take.
 bool paged_pieces_ok(const PagedP& p);
 
-// Few new tokens a sequence: at most 16 rows (tokens x query heads of a
-// group) per K/V head. Bytes of workspace after the status block, and the
+// Few new tokens a sequence: 16 or 32 rows (tokens x query heads of a group) per
+// K/V head at most, by a measured rule. Bytes of workspace after the status block, and the
 // launch itself, which sets the status word (nothing needs clearing).
 bool paged_decode_supported(const PagedP& p, int32_t max_q);
 size_t paged_decode_workspace_bytes();

@@ -230,6 +230,17 @@ def test_max_q_changes_no_set(kind):
     check(o, lse, *reference(q, K, V, c["new"], c["lens"], 128 ** -0.5), tensor_core=True)
 
 
+@pytest.mark.parametrize("mask", list(MASKS))
+@pytest.mark.parametrize("new", [[5, 6, 0, 2], [8, 1, 7, 8], [9, 8, 12, 3]])  # up to 24, 32 and 48 rows a K/V head
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+def test_several_row_blocks_of_drafted_tokens(new, mask, cd):
+    lens = [70, 8, 260, 129]
+    cache, K, V = make_cache(lens, 16, 2, 128, 128, DT[cd], seed=8, src=torch.bfloat16)
+    q = seeded_q(sum(new), 8, 128, torch.bfloat16, 9)
+    o, lse = run(q, cache, new, allowed=allowed_of(MASKS[mask]), max_q=max(new))
+    check(o, lse, *reference(q, K, V, new, lens, 128 ** -0.5, **MASKS[mask]), tensor_core=True, cache=cd)
+
+
 @pytest.mark.parametrize("kind,new", [("decode", 1), ("few_tokens", 3), ("chunk", 60)])
 @pytest.mark.parametrize("cd", ["bf16", "e4m3"])
 def test_rows_outside_every_sequence_and_strides(kind, new, cd):
