@@ -319,8 +319,8 @@ typedef struct attn_cache {
  * the other three: each row x is then stored as scale = max|x| / 448 (1 for a
  * row of zeros) and e4m3(x / scale), rounded to nearest even; a row that
  * holds an infinity or a NaN gets a non-finite scale and reads back as NaN
- * throughout. A page position must be written by one token only: pages
- * shared between sequences hold whichever token was stored last.
+ * throughout. A page position must be written by one token only: where two
+ * sequences' new tokens share one, its row may mix theirs.
  * workspace: NULL (device checks are then applied but not reported), or at
  * least 256 bytes for the status word. Caches of more than 2^30 positions a
  * sequence (max_pages * page_size), or more new tokens than that, are
