@@ -50,21 +50,26 @@ enum : uint8_t { kEmpty = 0, kFull = 1, kPartial = 2 };
 // causal/window band, and is any? Rows are given as key positions (query row
 // + qoff). Row i allows [max(c0, i-W+1), min(c1, i)], so some row qualifies
 // iff i can be chosen with c0 <= i (causal) and i <= c1 + W - 1 (window). The
-// window does not apply to columns below m.first (0 when not set).
+// window does not apply to columns below m.first (0 when not set; kFirst false
+// here and below: known to be 0, which the query-centric dQ pass uses: its
+// issuer walks the tiles between products, and the tests cost it 2 %).
+template <bool kFirst = true>
 __device__ __forceinline__ void band_test(const MaskP& m, int64_t r0, int64_t r1, int64_t c0, int64_t c1, bool& any,
                                           bool& all) {
   const bool causal = m.flags & ATTN_MASK_CAUSAL, window = m.flags & ATTN_MASK_WINDOW;
   all = true;
   if (causal && c1 > r0) all = false;
-  if (window && c1 >= m.first && (c0 > m.first ? c0 : m.first) < r1 - m.window + 1) all = false;
+  const int64_t first = kFirst ? m.first : 0;
+  if (window && c1 >= first && (c0 > first ? c0 : first) < r1 - m.window + 1) all = false;
   int64_t lo = r0, hi = r1;
   if (causal && c0 > lo) lo = c0;
   if (window && c1 + m.window - 1 < hi) hi = c1 + m.window - 1;
   any = c0 <= c1 && lo <= hi;
-  if (c0 < m.first && c0 <= c1 && r0 <= r1 && (!causal || c0 <= r1)) any = true;
+  if (kFirst && c0 < first && c0 <= c1 && r0 <= r1 && (!causal || c0 <= r1)) any = true;
 }
 
 // Class of the (64-row query slice qs, 128-key tile kt) pair.
+template <bool kFirst = true>
 __device__ uint8_t tile_class(const MaskP& m, int Tq, int Tk, int b, int h, int qs, int kt) {
   const int64_t r0 = (int64_t)qs * kBMb, r1 = (r0 + kBMb < Tq ? r0 + kBMb : Tq) - 1;
   const int64_t c0 = (int64_t)kt * kBN, c1e = c0 + kBN - 1, c1 = (c1e < Tk ? c1e : Tk - 1);
@@ -72,7 +77,7 @@ __device__ uint8_t tile_class(const MaskP& m, int Tq, int Tk, int b, int h, int 
   bool any = false, all = c1e <= Tk - 1;
   if (!(m.flags & ATTN_MASK_BLOCK)) {
     bool a, f;
-    band_test(m, r0 + m.qoff, r1 + m.qoff, c0, c1, a, f);
+    band_test<kFirst>(m, r0 + m.qoff, r1 + m.qoff, c0, c1, a, f);
     any = a;
     all = all && f;
   } else {
@@ -84,7 +89,7 @@ __device__ uint8_t tile_class(const MaskP& m, int Tq, int Tk, int b, int h, int 
         const int64_t cc0 = cb * m.bk > c0 ? cb * m.bk : c0;
         const int64_t cc1 = cb * m.bk + m.bk - 1 < c1 ? cb * m.bk + m.bk - 1 : c1;
         bool a, f;
-        band_test(m, rr0 + m.qoff, rr1 + m.qoff, cc0, cc1, a, f);
+        band_test<kFirst>(m, rr0 + m.qoff, rr1 + m.qoff, cc0, cc1, a, f);
         if (base[rb * m.bm_sq + cb]) {
           any = any || a;
           all = all && f;
@@ -138,10 +143,11 @@ struct ClassTable {
   int nqs, nkt;
 };
 
+template <bool kFirst = true>
 __device__ __forceinline__ uint8_t lookup_class(const ClassTable& ct, const MaskP& m, int Tq, int Tk, int b, int h,
                                                 int qs, int kt) {
   if ((int64_t)qs * kBMb >= Tq) return kEmpty;  // slices past the last row are not in the table
-  if (!ct.cls) return tile_class(m, Tq, Tk, b, h, qs, kt);
+  if (!ct.cls) return tile_class<kFirst>(m, Tq, Tk, b, h, qs, kt);
   const int sb = ct.nb > 1 ? b : 0, sh = ct.nh > 1 ? h : 0;
   return ct.cls[(((int64_t)sb * ct.nh + sh) * ct.nqs + qs) * ct.nkt + kt];
 }
@@ -160,10 +166,11 @@ __global__ void classify_kernel(MaskP m, int Tq, int Tk, int B, int Hq, ClassTab
 }
 
 // Forward tile class for a 128-row query tile: merge its two 64-row slices.
+template <bool kFirst = true>
 __device__ __forceinline__ uint8_t fwd_class(const ClassTable& ct, const MaskP& m, int Tq, int Tk, int b, int h,
                                              int qt, int kt) {
-  const uint8_t a = lookup_class(ct, m, Tq, Tk, b, h, 2 * qt, kt);
-  const uint8_t c = (2 * qt + 1) * kBMb < Tq ? lookup_class(ct, m, Tq, Tk, b, h, 2 * qt + 1, kt) : a;
+  const uint8_t a = lookup_class<kFirst>(ct, m, Tq, Tk, b, h, 2 * qt, kt);
+  const uint8_t c = (2 * qt + 1) * kBMb < Tq ? lookup_class<kFirst>(ct, m, Tq, Tk, b, h, 2 * qt + 1, kt) : a;
   if (a == kEmpty && c == kEmpty) return kEmpty;
   if (a == kFull && c == kFull) return kFull;
   return kPartial;
@@ -250,9 +257,10 @@ __device__ __forceinline__ FwdGap fwd_gap(const MaskP& m, int q0) {
 }
 
 // Class of (128-row query tile qt, key tile kt); tiles past Tq are empty.
+template <bool kFirst = true>
 __device__ __forceinline__ uint8_t wg_class(const FwdArgs& a, int b, int h, int qt, int kt) {
   if (qt * kBM >= a.Tq) return kEmpty;
-  return fwd_class(a.ct, a.m, a.Tq, a.Tk, b, h, qt, kt);
+  return fwd_class<kFirst>(a.ct, a.m, a.Tq, a.Tk, b, h, qt, kt);
 }
 
 // First key tile after `from` (up to kt_hi) with allowed keys for either
@@ -1463,18 +1471,19 @@ struct DqCtl {
 
 // Next key tile after `from` (up to kt_hi) with allowed keys for query tile
 // qt; kt_hi + 1 when none. Every role walks the same sequence.
+template <bool kFirst>
 __device__ __forceinline__ int dq_next_tile(const FwdArgs& a, int b, int h, int qt, const FwdGap& gap, int kt_hi,
                                             int from) {
   for (int kt = from + 1; kt <= kt_hi; ++kt) {
-    if (kt == gap.lo && (kt = gap.hi) > kt_hi) break;
-    if (wg_class(a, b, h, qt, kt) != kEmpty) return kt;
+    if (kFirst && kt == gap.lo && (kt = gap.hi) > kt_hi) break;
+    if (wg_class<kFirst>(a, b, h, qt, kt) != kEmpty) return kt;
   }
   return kt_hi + 1;
 }
 
-// kSum: each row's delta_i = sum_j p_ij <G_i, V_j> as well, in fp32 (the
+// kFirst: a window with first keys. kSum (with them only): each row's delta_i = sum_j p_ij <G_i, V_j> as well, in fp32 (the
 // prepare kernel's <G_i, Y_i> takes the stored, 16-bit Y).
-template <bool kH, bool kSum>
+template <bool kH, bool kFirst, bool kSum>
 __global__ void __launch_bounds__(kDqThreads, 1)
 dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg, const DqArgs a) {
@@ -1494,7 +1503,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
   const int q0 = qt * kBM;
   int kt_lo, kt_hi;
   fwd_key_tiles(f.m, b, f.Tq, f.Tk, q0, kBM, kt_lo, kt_hi);
-  const FwdGap gap = fwd_gap(f.m, q0);
+  const FwdGap gap = kFirst ? fwd_gap(f.m, q0) : FwdGap{-1, -1};
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ctl->q_full), 1);
@@ -1519,7 +1528,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int first = dq_next_tile(f, b, h, qt, gap, kt_hi, kt_lo - 1);
+  const int first = dq_next_tile<kFirst>(f, b, h, qt, gap, kt_hi, kt_lo - 1);
 
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer
@@ -1534,7 +1543,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     tma_load_4d(sbase + kDqG, &tg, qf, 0, q0, h, b);
     tma_load_4d(sbase + kDqG + kTileBytes / 2, &tg, qf, 64, q0, h, b);
     int n = 0;
-    for (int kt = first; kt <= kt_hi; kt = dq_next_tile(f, b, h, qt, gap, kt_hi, kt), ++n) {
+    for (int kt = first; kt <= kt_hi; kt = dq_next_tile<kFirst>(f, b, h, qt, gap, kt_hi, kt), ++n) {
       const int s = n % kStages;
       if (!wait_bar(smem_u32(&ctl->kv_empty[s]), ((n / kStages) & 1) ^ 1, abort_flag, f.status)) break;
       const uint32_t kf = smem_u32(&ctl->k_full[s]), vf = smem_u32(&ctl->v_full[s]);
@@ -1597,7 +1606,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
       }
     }
     for (int kt = first; ok && kt <= kt_hi; ++n) {
-      const int nk = dq_next_tile(f, b, h, qt, gap, kt_hi, kt);
+      const int nk = dq_next_tile<kFirst>(f, b, h, qt, gap, kt_hi, kt);
       const int s = n % kStages, s1 = (n + 1) % kStages;
       const bool more = nk <= kt_hi;
       if (more) {  // S of the next tile into the other buffer while the warps work on this one
@@ -1646,14 +1655,14 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     int cbase = kt_lo - 32;
     uint32_t cword = 0;
     for (int kt = kt_lo; ok && kt <= kt_hi; ++kt) {
-      if (kt == gap.lo && (kt = gap.hi) > kt_hi) break;
+      if (kFirst && kt == gap.lo && (kt = gap.hi) > kt_hi) break;
       if (kt - cbase >= 32) {
         cbase = kt;
         const int mk = kt + lane;
         cword = 0;
         if (mk <= kt_hi) {
-          cword = wg_class(f, b, h, qt, mk);
-          if (cword == kPartial) cword |= ((uint32_t)lookup_class(f.ct, f.m, f.Tq, f.Tk, b, h, slice, mk) & 3u) << 2;
+          cword = wg_class<kFirst>(f, b, h, qt, mk);
+          if (cword == kPartial) cword |= ((uint32_t)lookup_class<kFirst>(f.ct, f.m, f.Tq, f.Tk, b, h, slice, mk) & 3u) << 2;
         }
       }
       const uint32_t cv = __shfl_sync(0xffffffffu, cword, kt - cbase);
@@ -1970,10 +1979,11 @@ size_t bwd_split_bytes(const BwdSplit& sp, int B, int Hkv, int Tk) {
 
 // Raise a kernel's dynamic shared-memory limit once per device. which names
 // the kernel instantiation, one slot each: forward 0-3 and 6-7 (first keys),
-// query-centric dQ 4-5 and 20-21 (with row sums), reverse 8-15, split 16-19.
+// query-centric dQ 4-5, 20-21 (with row sums) and 22-23 (with first keys), reverse
+// 8-15, split 16-19.
 cudaError_t set_smem_attr(const void* fn, uint32_t bytes, int which) {
-  static bool done[22][64] = {};
-  if (which < 0 || which >= 22) return cudaErrorInvalidValue;
+  static bool done[24][64] = {};
+  if (which < 0 || which >= 24) return cudaErrorInvalidValue;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -2203,11 +2213,12 @@ cudaError_t sm100_dense_bwd(const DenseP& p, const void* o, const int64_t so[3],
     d.scale = p.scale;
     d.Tpad = Tpad;
     d.rowsum = exact_delta ? delta : nullptr;
-    auto kdq = exact_delta ? (f16 ? dq_kernel<true, true> : dq_kernel<false, true>)
-                           : (f16 ? dq_kernel<true, false> : dq_kernel<false, false>);
-    if ((err = set_smem_attr(reinterpret_cast<const void*>(kdq), kDqSmem, (exact_delta ? 20 : 4) + (f16 ? 1 : 0))) !=
-        cudaSuccess)
-      return err;
+    const bool first = p.m.first > 0;
+    auto kdq = exact_delta ? (f16 ? dq_kernel<true, true, true> : dq_kernel<false, true, true>)
+               : first     ? (f16 ? dq_kernel<true, true, false> : dq_kernel<false, true, false>)
+                           : (f16 ? dq_kernel<true, false, false> : dq_kernel<false, false, false>);
+    const int slot = (exact_delta ? 20 : first ? 22 : 4) + (f16 ? 1 : 0);
+    if ((err = set_smem_attr(reinterpret_cast<const void*>(kdq), kDqSmem, slot)) != cudaSuccess) return err;
     const int nqt = (p.Tq + kBM - 1) / kBM;
     kdq<<<nqt * p.B * p.Hq, kDqThreads, kDqSmem, st>>>(dq_mq, mk, mv, dq_mg, d);
     return cudaGetLastError();
