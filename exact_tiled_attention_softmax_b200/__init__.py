@@ -99,7 +99,8 @@ def load_library():
         raise RuntimeError(f"CUDA library not built: {path} is missing "
                            "(run python -m exact_tiled_attention_softmax_b200.build)")
     lib = ctypes.CDLL(path)
-    T, M, vp, sz = ctypes.POINTER(AttnTensorC), ctypes.POINTER(AttnMaskC), ctypes.c_void_p, ctypes.c_size_t
+    M, vp, sz = ctypes.POINTER(AttnMaskC), ctypes.c_void_p, ctypes.c_size_t
+    T = C = vp  # attn_tensor and attn_cache descriptors: packed bytes, or a structure by reference
     lib.attn_version.restype = ctypes.c_int
     lib.attn_status_string.restype = ctypes.c_char_p
     lib.attn_status_string.argtypes = [ctypes.c_int]
@@ -113,15 +114,14 @@ def load_library():
     lib.attn_bwd.argtypes = [T, T, T, T, T, T, M, ctypes.c_float, T, T, T, vp, vp, sz, vp]
     lib.attn_bwd_noalloc.restype = ctypes.c_int
     lib.attn_bwd_noalloc.argtypes = [T, T, T, T, T, T, M, ctypes.c_float, T, T, T, vp, vp]
-    # Descriptors of the paged calls go as packed bytes (or by reference).
     lib.attn_cache_write.restype = ctypes.c_int
-    lib.attn_cache_write.argtypes = [vp, vp, vp, vp, vp, sz, vp]
+    lib.attn_cache_write.argtypes = [T, T, vp, C, vp, sz, vp]
     lib.attn_cache_read.restype = ctypes.c_int
-    lib.attn_cache_read.argtypes = [vp, vp, vp, vp, sz, vp]
+    lib.attn_cache_read.argtypes = [C, T, T, vp, sz, vp]
     lib.attn_paged_workspace_size.restype = sz
-    lib.attn_paged_workspace_size.argtypes = [vp, vp, M]
+    lib.attn_paged_workspace_size.argtypes = [T, C, M]
     lib.attn_paged_fwd.restype = ctypes.c_int
-    lib.attn_paged_fwd.argtypes = [vp, vp, vp, M, ctypes.c_float, ctypes.c_int32, vp, vp, vp, sz, vp]
+    lib.attn_paged_fwd.argtypes = [T, vp, C, M, ctypes.c_float, ctypes.c_int32, T, T, vp, sz, vp]
     lib.attn_get_status.restype = ctypes.c_int
     lib.attn_get_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.attn_selftest_wait_timeout.restype = ctypes.c_int
@@ -168,16 +168,9 @@ def _fields(t: torch.Tensor) -> tuple:
     return (t.data_ptr() if t.numel() else 0, _DTYPES.get(t.dtype, -1), n, *t.shape, *pad, *t.stride(), *pad)
 
 
-def _packed(t: torch.Tensor) -> bytes:
-    return _TENSOR.pack(*_fields(t))
-
-
-def _tensor(t: torch.Tensor | None):
-    return None if t is None else AttnTensorC.from_buffer_copy(_packed(t))
-
-
-def _ref(c):
-    return c  # ctypes passes a structure to a pointer argument by reference
+def _packed(t: torch.Tensor | None) -> bytes | None:
+    """The attn_tensor of t (NULL for None)."""
+    return None if t is None else _TENSOR.pack(*_fields(t))
 
 
 def _check_on(device: torch.device, *tensors) -> None:
@@ -327,15 +320,15 @@ def _is_topk(allowed: AllowedSet | None) -> bool:
 
 
 def attn_fwd_workspace_size(q, k, v, allowed: AllowedSet | None = None) -> int:
-    cq, ck, cv = _tensor(q), _tensor(k), _tensor(v)
+    cq, ck, cv = _packed(q), _packed(k), _packed(v)
     m = allowed.to_c() if allowed else None
-    return int(load_library().attn_fwd_workspace_size(_ref(cq), _ref(ck), _ref(cv), _ref(m)))
+    return int(load_library().attn_fwd_workspace_size(cq, ck, cv, m))
 
 
 def attn_bwd_workspace_size(q, k, v, allowed: AllowedSet | None = None) -> int:
-    cq, ck, cv = _tensor(q), _tensor(k), _tensor(v)
+    cq, ck, cv = _packed(q), _packed(k), _packed(v)
     m = allowed.to_c() if allowed else None
-    return int(load_library().attn_bwd_workspace_size(_ref(cq), _ref(ck), _ref(cv), _ref(m)))
+    return int(load_library().attn_bwd_workspace_size(cq, ck, cv, m))
 
 
 def attn_fwd(q, k, v, allowed: AllowedSet | None = None, scale: float | None = None, *,
@@ -352,12 +345,12 @@ def attn_fwd(q, k, v, allowed: AllowedSet | None = None, scale: float | None = N
     if lse is None:
         lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
     m = allowed.to_c() if allowed else None
-    cq, ck, cv, co, cl = (_tensor(x) for x in (q, k, v, out, lse))
-    need = lib.attn_fwd_workspace_size(_ref(cq), _ref(ck), _ref(cv), _ref(m))
+    cq, ck, cv, co, cl = (_packed(x) for x in (q, k, v, out, lse))
+    need = lib.attn_fwd_workspace_size(cq, ck, cv, m)
     if workspace is None:
         workspace = _workspace(need, q.device)
     _check_on(q.device, k, v, out, lse, workspace, *(allowed.tensors() if allowed else ()))
-    rc = lib.attn_fwd(_ref(cq), _ref(ck), _ref(cv), _ref(m), ctypes.c_float(scale), _ref(co), _ref(cl),
+    rc = lib.attn_fwd(cq, ck, cv, m, scale, co, cl,
                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd")
@@ -381,15 +374,15 @@ def attn_bwd(q, k, v, o, do, lse, allowed: AllowedSet | None = None, scale: floa
     if dsink is None and allowed is not None and allowed.sink is not None:
         dsink = torch.empty_like(allowed.sink, dtype=torch.float32)
     m = allowed.to_c() if allowed else None
-    cq, ck, cv, co, cdo, cl = (_tensor(x) for x in (q, k, v, o, do, lse))
-    cdq, cdk, cdv = _tensor(dq), _tensor(dk), _tensor(dv)
-    need = lib.attn_bwd_workspace_size(_ref(cq), _ref(ck), _ref(cv), _ref(m))
+    cq, ck, cv, co, cdo, cl = (_packed(x) for x in (q, k, v, o, do, lse))
+    cdq, cdk, cdv = _packed(dq), _packed(dk), _packed(dv)
+    need = lib.attn_bwd_workspace_size(cq, ck, cv, m)
     if workspace is None:
         workspace = _workspace(need, q.device)
     _check_on(q.device, k, v, o, do, lse, dq, dk, dv, dsink, workspace,
               *(allowed.tensors() if allowed else ()))
-    rc = lib.attn_bwd(_ref(cq), _ref(ck), _ref(cv), _ref(co), _ref(cdo), _ref(cl), _ref(m),
-                      ctypes.c_float(scale), _ref(cdq), _ref(cdk), _ref(cdv),
+    rc = lib.attn_bwd(cq, ck, cv, co, cdo, cl, m,
+                      scale, cdq, cdk, cdv,
                       dsink.data_ptr() if dsink is not None else None,
                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
     if rc != ATTN_OK:
@@ -407,11 +400,11 @@ def attn_bwd_noalloc(q, k, v, o, do, lse, allowed: AllowedSet | None = None, sca
     if scale is None:
         scale = q.shape[-1] ** -0.5
     m = allowed.to_c() if allowed else None
-    cq, ck, cv, co, cdo, cl = (_tensor(x) for x in (q, k, v, o, do, lse))
-    cdq, cdk, cdv = _tensor(dq), _tensor(dk), _tensor(dv)
+    cq, ck, cv, co, cdo, cl = (_packed(x) for x in (q, k, v, o, do, lse))
+    cdq, cdk, cdv = _packed(dq), _packed(dk), _packed(dv)
     _check_on(q.device, k, v, o, do, lse, dq, dk, dv, dsink, *(allowed.tensors() if allowed else ()))
-    rc = lib.attn_bwd_noalloc(_ref(cq), _ref(ck), _ref(cv), _ref(co), _ref(cdo), _ref(cl), _ref(m),
-                              ctypes.c_float(scale), _ref(cdq), _ref(cdk), _ref(cdv),
+    rc = lib.attn_bwd_noalloc(cq, ck, cv, co, cdo, cl, m,
+                              scale, cdq, cdk, cdv,
                               dsink.data_ptr() if dsink is not None else None, _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_bwd_noalloc")
