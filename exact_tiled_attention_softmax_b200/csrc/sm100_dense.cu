@@ -1782,8 +1782,13 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         }
       }
     }
-    // Every product has read the Q tile by now (dq_final, or there was none).
-    if constexpr (kSum) reinterpret_cast<float*>(smem + kDqQ)[w * kBM + t] = ok ? dsum : 0.f;
+    // The row sums go where the Q tile was: every product has read it by now
+    // (dq_final), and where there was none its copy, which is issued all the
+    // same, must have landed, or it would overwrite them.
+    if constexpr (kSum) {
+      if (n == 0) wait_bar(smem_u32(&ctl->q_full), 0, abort_flag, f.status);
+      reinterpret_cast<float*>(smem + kDqQ)[w * kBM + t] = ok ? dsum : 0.f;
+    }
   }
   tc_fence_before();
   __syncthreads();

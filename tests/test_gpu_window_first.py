@@ -144,6 +144,49 @@ def test_sink_gradient_is_fp32_accurate(dtype):
     assert (np.abs(to_np(dsink) - bw.dsink) <= 2.0 ** -17 * size).all(), (to_np(dsink) - bw.dsink, size)
 
 
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("kind", ["lengths", "shorter_keys", "block"])
+def test_sink_gradient_with_query_tiles_that_see_no_key(kind, dtype, deterministic):
+    """Rows without a key give the sink all of their probability and no
+    gradient (delta 0), whole 128-row tiles of them too: a batch row of length
+    0, queries in front of the first key, an all-zero stripe of the block mask.
+    The bound is test_sink_gradient_is_fp32_accurate's; such rows add nothing to it."""
+    B, Hq, Hkv, W_, F, d = 3, 4, 2, 60, 9, 128
+    Tq, Tk = (700, 350) if kind == "shorter_keys" else (600, 600)
+    lengths = [600, 0, 200] if kind == "lengths" else None
+    block, bm = 64, None
+    rng = np.random.default_rng(31)
+    if kind == "block":
+        bm = (rng.random((B, Hq, -(-Tq // block), -(-Tk // block))) < 0.6).astype(np.uint8)
+        bm[:, :, 2:6] = 0  # query rows 128 .. 383
+    f = lambda s: W.round_to_storage(rng.standard_normal(s, dtype=np.float32), dtype)  # noqa: E731
+    q, k, v, g = f((B, Hq, Tq, d)), f((B, Hkv, Tk, d)), f((B, Hkv, Tk, d)), f((B, Hq, Tq, d))
+    sink = rng.standard_normal(Hq).astype(np.float32)
+    tq, tk, tv, tg = (to_dev(x, TORCH_DTYPE[dtype]) for x in (q, k, v, g))
+    allowed = eta.AllowedSet(
+        causal=True, window_left=W_, window_first=F, sink=to_dev(sink, torch.float32), deterministic=deterministic,
+        block_mask=to_dev(bm, torch.uint8) if bm is not None else None, block_q=block, block_k=block,
+        lengths=torch.tensor(lengths, dtype=torch.int32, device="cuda") if lengths else None)
+    wb = torch.empty(eta.attn_bwd_workspace_size(tq, tk, tv, allowed), dtype=torch.uint8, device="cuda")
+    o, lse = eta.attn_fwd(tq, tk, tv, allowed)
+    dq, dk, dv, dsink = eta.attn_bwd(tq, tk, tv, o, tg, lse, allowed, workspace=wb)
+    assert eta.attn_get_status(wb) == 0
+    allow = allow_grid(Tq, Tk, window=W_, first=F, lengths=lengths, bm=bm, block=block)
+    q, k, v, g = (x.astype(np.float64) for x in (q, k, v, g))
+    z = sink.astype(np.float64)
+    fw = oracle.forward(q, k, v, allow, d ** -0.5, sink=z)
+    bw = oracle.backward(q, k, v, g, allow, d ** -0.5, sink=z, y=fw.y)
+    for name, got, want in (("dq", dq, bw.dq), ("dk", dk, bw.dk), ("dv", dv, bw.dv)):
+        check_close(name, to_np(got), want, fp32=False, grad=True, storage=dtype)
+    kk, vv = np.repeat(k, Hq // Hkv, 1), np.repeat(v, Hq // Hkv, 1)
+    s = np.where(allow, np.einsum("bhid,bhjd->bhij", q, kk) * d ** -0.5, -np.inf)
+    assert np.isneginf(s).all(-1).reshape(B, Hq, -1)[:, :, :Tq // 128 * 128].reshape(B, Hq, -1, 128).all(-1).any()
+    p = np.exp(s - fw.lse[..., None])
+    size = (np.exp(sink[:, None] - fw.lse) * (p * np.abs(np.einsum("bhid,bhjd->bhij", g, vv))).sum(-1)).sum((0, 2))
+    assert (np.abs(to_np(dsink) - bw.dsink) <= 2.0 ** -17 * size).all(), (to_np(dsink) - bw.dsink, size)
+
+
 def test_gradients_against_differences():
     """fp32, autograd: <grad, u> against a central difference along u. With
     h = 2^-6 the difference's own error is h^2/6 times a third derivative
