@@ -324,6 +324,7 @@ struct PagedCtl {
   uint64_t k_full[kPStages], v_full[kPStages], v_ok[kPStages], kv_empty[kPStages];
   uint64_t s_full[2], p_full[2];
   uint64_t o_final;
+  uint64_t o_read;  // one arrival per softmax warp: it has passed o_final and read the mark
   uint32_t tmem_base;
   uint32_t abort_flag;
   uint32_t odd_piece;  // 1 + the piece whose V tiles lost non-finite elements
@@ -622,6 +623,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       mbar_init(smem_u32(&ctl->p_full[s]), 4);
     }
     mbar_init(smem_u32(&ctl->o_final), 1);
+    mbar_init(smem_u32(&ctl->o_read), 8);
     ctl->abort_flag = 0;
     ctl->odd_piece = 0;
     fence_barrier_init();
@@ -754,13 +756,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       hv.init(p, it);
       uint32_t cls;
       const bool any = next_seen(it, hv, k0, k1, cls) < k1;
+      // A piece begins once every softmax warp has passed the previous one's
+      // o_final, whether the piece has tiles (or its half has) or not: o_final is
+      // waited for by its parity, so nobody may be two of its phases behind.
+      if (piece > 0 && !(ok = wait_all(&ctl->o_read, (piece - 1) & 1))) break;
       if (q_boxes) {
-        // Q, once the previous piece's products have read the last one: two
+        // Q (the previous piece's products have read the last one: o_final): two
         // boxes of (64 columns, the group's heads, 128 / group tokens) a half.
         // Rows past the block's belong to other tokens; their results go
         // nowhere. The softmax warps may still be writing the previous piece:
         // its O and this piece's S are different columns.
-        if (piece > 0 && !(ok = wait_all(&ctl->o_final, (piece - 1) & 1))) break;
         if (leader) {
           const uint32_t qf = smem_u32(&ctl->q_full);
           const int group = p.Hq / c.Hkv, halves = it.rows > 128 ? 2 : 1;
@@ -1130,6 +1135,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       // ---- epilogue: the rows, or this piece's part of them
       const bool whole = k0 == 0 && k1 == it.tiles;
       const bool odd = *reinterpret_cast<volatile uint32_t*>(&ctl->odd_piece) == (uint32_t)piece + 1u;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->o_read));
       int64_t tok;
       int h;
       row_place(p, it, valid ? rr : 0, tok, h);

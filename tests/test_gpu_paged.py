@@ -307,6 +307,25 @@ def test_empty_rows_and_bad_pages(kind, new, cd):
         check(o[empty:], lse[empty:], *t, tensor_core=True, cache=cd)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (9, 3)])
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+def test_many_row_blocks_without_keys(Hq, Hkv, cd):
+    """Sequences of length 0 that bring thousands of tokens: every CTA walks
+    several row blocks without a key, between blocks of a sequence that has
+    keys. All are reported, none delays or disturbs the others."""
+    new, lens = [16384, 600, 8192], [0, 900, 0]
+    cache, K, V = make_cache(lens, 16, Hkv, 128, 128, DT[cd], seed=15, src=torch.bfloat16)
+    q = seeded_q(sum(new), Hq, 128, torch.bfloat16, 16)
+    a = eta.AllowedSet(causal=True)
+    o, lse = run(q, cache, new, allowed=a, max_q=max(new), status=eta.ATTN_DEVERR_RAGGED)
+    at = slice(new[0], new[0] + new[1])
+    check(o[at], lse[at], *reference(q[at], K[1:2], V[1:2], new[1:2], lens[1:2], 128 ** -0.5), tensor_core=True, cache=cd)
+    for part in (slice(0, new[0]), slice(new[0] + new[1], None)):
+        assert (o[part] == 0).all() and (lse[part] == -math.inf).all()
+    o2, lse2 = run(q, cache, new, allowed=a, max_q=max(new), status=eta.ATTN_DEVERR_RAGGED)
+    assert torch.equal(bits(o), bits(o2)) and torch.equal(bits(lse), bits(lse2))
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("kind,new", [("decode", 1), ("few", 4), ("chunk", 150), ("any", 4)])
 def test_masked_rows_hold_anything(kind, new, value):
