@@ -324,10 +324,11 @@ struct PagedCtl {
   uint64_t k_full[kPStages], v_full[kPStages], v_ok[kPStages], kv_empty[kPStages];
   uint64_t s_full[2], p_full[2];
   uint64_t o_final;
-  uint64_t o_read;  // one arrival per softmax warp: it has passed o_final and read the mark
+  uint64_t o_read;  // one arrival per softmax warp: it has passed o_final and read `lost`
   uint32_t tmem_base;
   uint32_t abort_flag;
-  uint32_t odd_piece;  // 1 + the piece whose V tiles lost non-finite elements
+  uint32_t lost;                   // the piece's V tiles lost non-finite elements (set before o_final)
+  uint32_t tile_lost[kPStages][4]; // the same per stage and checker warp (before v_ok)
   // e4m3, by 32 keys: the K scales' extremes, and the power of two (its
   // logarithm) that V's scales were divided by.
   float ks_top[kPStages][4], ks_low[kPStages][4], v_exp[kPStages][4];
@@ -622,10 +623,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       mbar_init(smem_u32(&ctl->s_full[s]), 1);
       mbar_init(smem_u32(&ctl->p_full[s]), 4);
     }
-    mbar_init(smem_u32(&ctl->o_final), 1);
+    mbar_init(smem_u32(&ctl->o_final), 2);  // the products' completion, and the word in front of it
     mbar_init(smem_u32(&ctl->o_read), 8);
     ctl->abort_flag = 0;
-    ctl->odd_piece = 0;
+    ctl->lost = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -784,7 +785,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         break;
       }
       tc_fence_after();
-      uint32_t info = 0;
+      uint32_t info = 0, lost = 0;
       int npv[2] = {0, 0};
       if (any) {
         const int s = n % kPStages;
@@ -824,6 +825,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           }
         }
         if (!ok) break;
+        lost |= __any_sync(0xffffffffu, lane < M::kCheckers && ctl->tile_lost[s][lane] != 0u);
         if (leader) mma_commit(smem_u32(&ctl->kv_empty[s]));
         __syncwarp();
         ++n;
@@ -831,7 +833,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         info = ninfo;
       }
       if (!ok) break;
-      if (leader) mma_commit(smem_u32(&ctl->o_final));
+      if (leader) {
+        ctl->lost = lost;  // (the softmax warps have read the previous piece's: o_read)
+        mbar_arrive(smem_u32(&ctl->o_final));
+        mma_commit(smem_u32(&ctl->o_final));
+      }
       __syncwarp();
       ++piece;
     }
@@ -839,7 +845,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // ---------------- checkers (e4m3: converters): V's non-finite elements, and
     // an e4m3 tile's 16-bit form
     const int ci = kQ8 ? warp - 12 : warp - 2;
-    int n = 0, piece = 0;
+    int n = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, wait_bar(smem_u32(bar), par, abort_flag, status));
@@ -1005,14 +1011,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           }
           fence_proxy_async_smem();
         }
-        if (__any_sync(0xffffffffu, odd)) {
-          // Rare. The mark is set while this piece's rows are being worked on:
-          // after their Q came, before the last of this tile's products.
-          if (!(ok = wait_all(&ctl->q_full, piece & 1))) break;
-          if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&ctl->odd_piece) = (uint32_t)piece + 1u;
-        }
-        __syncwarp();
+        // The mark goes with the tile: this warp may be pieces ahead of the
+        // products, so the issuing warp gathers the marks of a piece's tiles.
+        odd = __any_sync(0xffffffffu, odd);
         if (lane == 0) {
+          ctl->tile_lost[s][ci] = odd ? 1u : 0u;
           mbar_arrive(smem_u32(&ctl->v_ok[s]));
           if constexpr (kQ8) mbar_arrive(smem_u32(&ctl->raw_empty[1]));
         }
@@ -1022,7 +1025,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         nk = nnk;
         ncls = nncls;
       }
-      ++piece;
     }
   } else if (warp >= 4) {
     // ---------------- softmax warpgroups: warps 4-7 and 8-11, thread t of
@@ -1134,7 +1136,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       tc_fence_after();
       // ---- epilogue: the rows, or this piece's part of them
       const bool whole = k0 == 0 && k1 == it.tiles;
-      const bool odd = *reinterpret_cast<volatile uint32_t*>(&ctl->odd_piece) == (uint32_t)piece + 1u;
+      const bool odd = *reinterpret_cast<volatile uint32_t*>(&ctl->lost) != 0u;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->o_read));
       int64_t tok;

@@ -380,6 +380,58 @@ def test_masked_e4m3_rows_hold_anything(kind, new):
     assert not torch.isfinite(o[~ok.cuda()][:, 70]).any()
 
 
+def causal_reference(q, K, V, new, lens, scale):
+    """`reference` of causal rows that all see a key, whole matrices at a time."""
+    o, lse, A = [], [], []
+    for b, at in enumerate(cu_of(new, "cpu")[:-1].tolist()):
+        n, L, g = new[b], lens[b], q.shape[1] // K[b].shape[1]
+        k, v = (x[b].transpose(0, 1).repeat_interleave(g, 0) for x in (K, V))  # [Hq, L, d]
+        s = q[at:at + n].double().cpu().transpose(0, 1) @ k.transpose(1, 2) * scale
+        s = s.masked_fill(torch.arange(L) > torch.arange(L - n, L)[:, None], -math.inf)
+        m = torch.logsumexp(s, -1)
+        p = torch.exp(s - m[..., None])
+        for x, y in ((o, p @ v), (A, p @ v.abs()), (lse, m)):
+            x.append(y.transpose(0, 1))
+    return torch.cat(o), torch.cat(lse), torch.cat(A)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (12, 4)])
+@pytest.mark.parametrize("cd", ["bf16", "f16", "e4m3"])
+def test_non_finite_values_where_a_cta_walks_many_blocks(Hq, Hkv, cd):
+    """Hundreds of row blocks, of more and of less than 128 rows and many of one
+    key tile, with NaN and infinities in the last (partly visible) tiles and in
+    front of the new tokens of every third sequence: every row that sees one is
+    not finite, every other row is within its bound."""
+    g = torch.Generator().manual_seed(17)
+    B = 100
+    new = [int(x) for x in torch.randint(1, 60, (B,), generator=g)]
+    lens = [n + int(x) for n, x in zip(new, torch.randint(0, 130, (B,), generator=g))]
+    for b, (n, more) in enumerate([(300, 400), (140, 0), (257, 900), (131, 129)]):
+        new[30 * b], lens[30 * b] = n, n + more
+    qd = torch.float16 if cd == "f16" else torch.bfloat16
+    cache, K, V = make_cache(lens, 16, Hkv, 128, 128, DT[cd], seed=18, src=qd)
+    q = seeded_q(sum(new), Hq, 128, qd, 19)
+    head, group = Hkv - 1, Hq // Hkv
+    ok, at = torch.ones(sum(new), Hq, dtype=torch.bool), 0
+    for b, (n, L) in enumerate(zip(new, lens)):
+        if b % 3 == 0:
+            for i, j in enumerate({L - 1, max(0, L - 7), max(0, L - n - 3)} if b % 2 else {L - 1 - n // 2}):
+                pg, off = int(cache.block_table[b, j // 16]), j % 16
+                if cd != "e4m3":
+                    cache.v[pg, off, head, 70] = (math.nan, math.inf, -math.inf)[(i + b) % 3]
+                elif (i + b) % 2:
+                    cache.v.view(torch.uint8)[pg, off, head, 70] = 0xFF
+                else:
+                    cache.v_scale[pg, off, head] = math.inf
+                first = max(0, j - (L - n))  # the first new token that sees key j
+                ok[at + first:at + n, head * group:] = False
+        at += n
+    o, lse = run(q, cache, new, allowed=eta.AllowedSet(causal=True), max_q=max(new))
+    ref = causal_reference(q, K, V, new, lens, 128 ** -0.5)
+    check(o[ok.cuda()], lse[ok.cuda()], *[r[ok] for r in ref], tensor_core=True, cache=cd)
+    assert not torch.isfinite(o[~ok.cuda()][:, 70]).any()
+
+
 @pytest.mark.parametrize("new,kind", [(1, "decode"), (20, "chunk")])
 @pytest.mark.parametrize("cd", ["bf16", "e4m3"])
 def test_one_long_sequence_is_joined_from_many_shares(new, kind, cd):
