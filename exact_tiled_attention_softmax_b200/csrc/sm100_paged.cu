@@ -324,11 +324,12 @@ struct PagedCtl {
   uint64_t k_full[kPStages], v_full[kPStages], v_ok[kPStages], kv_empty[kPStages];
   uint64_t s_full[2], p_full[2];
   uint64_t o_final;
-  uint64_t o_read;  // one arrival per softmax warp: it has passed o_final and read `lost`
+  uint64_t o_read;  // one arrival per softmax warp: it has passed o_final and read lost_lo, lost_hi
   uint32_t tmem_base;
   uint32_t abort_flag;
-  uint32_t lost;                   // the piece's V tiles lost non-finite elements (set before o_final)
-  uint32_t tile_lost[kPStages][4]; // the same per stage and checker warp (before v_ok)
+  // 1 + k of the tiles whose V lost non-finite elements, 0 none: by stage and
+  // checker warp (set before v_ok), and the piece's first and last (before o_final).
+  uint32_t tile_lost[kPStages][4], lost_lo, lost_hi;
   // e4m3, by 32 keys: the K scales' extremes, and the power of two (its
   // logarithm) that V's scales were divided by.
   float ks_top[kPStages][4], ks_low[kPStages][4], v_exp[kPStages][4];
@@ -586,9 +587,87 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
   return alpha;
 }
 
-__device__ __forceinline__ float ldf16(const uint16_t* p, bool f16) {
-  const uint16_t v = *p;
-  return f16 ? __half2float(*reinterpret_cast<const __half*>(&v)) : __uint_as_float((uint32_t)v << 16);
+// Columns 32 ch + e (bit e) of the calling thread's row that get a NaN, +inf or
+// -inf back: the non-finite elements that the checkers took out of V, of the
+// keys that the row sees. By a whole warp, which owns 32 rows of the block: of
+// the tiles in [k0, k1) that lose any (seen in part, or with a box outside
+// the pool) each lane looks at one key in 32, and every key that has some is
+// shown to all rows. Few tiles are seen in part; with the rows' keys one after
+// another, and in every tile of the piece, a chunk of a million keys would have
+// taken seconds for one NaN, and the other roles' waits would have run out.
+struct LostColumns {
+  uint32_t nan, up, down;
+};
+
+template <bool kH, bool kQ8>
+__device__ __forceinline__ LostColumns lost_columns(const PagedP& p, const Item& it, const Halves& hv, int k0, int k1,
+                                                    int pos, bool valid, int box, int ch) {
+  const CacheP& c = p.c;
+  const int lane = threadIdx.x & 31;
+  LostColumns lost{0u, 0u, 0u};
+  if (!__any_sync(0xffffffffu, valid)) return lost;
+  uint32_t cls;
+  auto page_at = [&](int j) {  // -1: past the end or outside the pool
+    if (j >= hv.L) return -1;
+    const int pg = c.table[(int64_t)it.b * c.table_stride + (unsigned)j / (unsigned)c.page_size];
+    return pg < c.num_pages ? pg : -1;
+  };
+#pragma unroll 1
+  for (int k = next_seen(it, hv, k0, k1, cls); k < k1; k = next_seen(it, hv, k + 1, k1, cls)) {
+    const int j0 = it.tile_at(k) * kPTile;
+    if (!in_part(cls)) {
+      const int j = j0 + lane * box;
+      if (!__any_sync(0xffffffffu, lane * box < kPTile && j < hv.L && page_at(j) < 0)) continue;
+    }
+    uint64_t w0, w1;
+    row_bits(hv, pos, valid, it.tile_at(k), 0u, box, w0, w1);
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t sees = (uint32_t)((q < 2 ? w0 : w1) >> (32 * (q & 1)));
+      const int j = j0 + 32 * q + lane, pg = page_at(j);
+      uint32_t nan = 0u, up = 0u, down = 0u;
+      if (pg >= 0) {
+        const int64_t off = (unsigned)j % (unsigned)c.page_size;
+        const int64_t at = pg * c.sv[0] + off * c.sv[1] + (int64_t)it.h * c.sv[2] + ch * 32;
+        const float vs = kQ8 ? c.vs[pg * c.svs[0] + off * c.svs[1] + (int64_t)it.h * c.svs[2]] : 1.f;
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(c.v) + at * (kQ8 ? 1 : 2));
+#pragma unroll 4
+        for (int i = 0; i < (kQ8 ? 8 : 16); ++i) {
+          const uint32_t v = row[i];
+          float x[4];
+          if constexpr (kQ8) {
+            const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
+            const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v >> 16), __NV_E4M3);
+            const float2 f0 = __half22float2(__half2(a)), f1 = __half22float2(__half2(b));
+            x[0] = f0.x * vs, x[1] = f0.y * vs, x[2] = f1.x * vs, x[3] = f1.y * vs;
+          } else {
+            const float2 f = unpack16<kH>(v);
+            x[0] = f.x, x[1] = f.y;
+          }
+#pragma unroll
+          for (int e = 0; e < (kQ8 ? 4 : 2); ++e) {
+            const uint32_t bit = 1u << ((kQ8 ? 4 : 2) * i + e);
+            if (x[e] != x[e]) nan |= bit;
+            if (x[e] == INFINITY) up |= bit;
+            if (x[e] == -INFINITY) down |= bit;
+          }
+        }
+      }
+      uint32_t keys = __ballot_sync(0xffffffffu, (nan | up | down) != 0u);
+      while (keys) {
+        const int src = __ffs(keys) - 1;
+        keys &= keys - 1;
+        const uint32_t a = __shfl_sync(0xffffffffu, nan, src), b = __shfl_sync(0xffffffffu, up, src),
+                       d = __shfl_sync(0xffffffffu, down, src);
+        if ((sees >> src) & 1u) {
+          lost.nan |= a;
+          lost.up |= b;
+          lost.down |= d;
+        }
+      }
+    }
+  }
+  return lost;
 }
 
 template <bool v>
@@ -626,7 +705,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     mbar_init(smem_u32(&ctl->o_final), 2);  // the products' completion, and the word in front of it
     mbar_init(smem_u32(&ctl->o_read), 8);
     ctl->abort_flag = 0;
-    ctl->lost = 0;
+    ctl->lost_lo = ctl->lost_hi = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -785,7 +864,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         break;
       }
       tc_fence_after();
-      uint32_t info = 0, lost = 0;
+      uint32_t info = 0, lost_lo = 0, lost_hi = 0;
       int npv[2] = {0, 0};
       if (any) {
         const int s = n % kPStages;
@@ -825,7 +904,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           }
         }
         if (!ok) break;
-        lost |= __any_sync(0xffffffffu, lane < M::kCheckers && ctl->tile_lost[s][lane] != 0u);
+        const uint32_t lost = __reduce_max_sync(0xffffffffu, lane < M::kCheckers ? ctl->tile_lost[s][lane] : 0u);
+        if (lost) {
+          if (!lost_lo) lost_lo = lost;
+          lost_hi = lost;
+        }
         if (leader) mma_commit(smem_u32(&ctl->kv_empty[s]));
         __syncwarp();
         ++n;
@@ -834,7 +917,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       if (!ok) break;
       if (leader) {
-        ctl->lost = lost;  // (the softmax warps have read the previous piece's: o_read)
+        ctl->lost_lo = lost_lo;  // (the softmax warps have read the previous piece's: o_read)
+        ctl->lost_hi = lost_hi;
         mbar_arrive(smem_u32(&ctl->o_final));
         mma_commit(smem_u32(&ctl->o_final));
       }
@@ -1015,7 +1099,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // products, so the issuing warp gathers the marks of a piece's tiles.
         odd = __any_sync(0xffffffffu, odd);
         if (lane == 0) {
-          ctl->tile_lost[s][ci] = odd ? 1u : 0u;
+          ctl->tile_lost[s][ci] = odd ? (uint32_t)k + 1u : 0u;
           mbar_arrive(smem_u32(&ctl->v_ok[s]));
           if constexpr (kQ8) mbar_arrive(smem_u32(&ctl->raw_empty[1]));
         }
@@ -1136,7 +1220,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       tc_fence_after();
       // ---- epilogue: the rows, or this piece's part of them
       const bool whole = k0 == 0 && k1 == it.tiles;
-      const bool odd = *reinterpret_cast<volatile uint32_t*>(&ctl->lost) != 0u;
+      const int lost0 = (int)*reinterpret_cast<volatile uint32_t*>(&ctl->lost_lo) - 1;  // -1: none
+      const int lost1 = (int)*reinterpret_cast<volatile uint32_t*>(&ctl->lost_hi);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->o_read));
       int64_t tok;
@@ -1148,6 +1233,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       float* slot = split_slot<kPRows, kPD>(SplitP{0, 0, nullptr, pl.part}, blockIdx.x, k0 == 0 ? 1 : 0);
 #pragma unroll 1
       for (int ch = 0; ch < 4; ++ch) {
+        LostColumns lost{0u, 0u, 0u};
+        if (lost0 >= 0) lost = lost_columns<kH, kQ8>(p, it, hv, lost0, lost1, pos, valid, box, ch);
         uint32_t o[32];
         if (got > 0) {
           tmem_ld32(tO + ch * 32, o);
@@ -1156,28 +1243,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           if (got == 0 || l_run == 0.f) o[e] = 0u;
-        if (odd) {  // non-finite V elements that the checkers took out, of the keys that this row sees
-          uint32_t c2;
-#pragma unroll 1
-          for (int k = next_seen(it, hv, k0, k1, c2); k < k1; k = next_seen(it, hv, k + 1, k1, c2)) {
-            const int kt = it.tile_at(k);
-            uint64_t w0, w1;
-            row_bits(hv, pos, valid, kt, 0u, box, w0, w1);
-#pragma unroll 1
-            for (int j = 0; j < kPTile; ++j) {
-              if (!(((j < 64 ? w0 : w1) >> (j & 63)) & 1ull)) continue;
-              const int64_t key = (int64_t)kt * kPTile + j;
-              const int64_t pg = page_of(c, it.b, key);
-              if (pg < 0) continue;
-              const int64_t at = pg * c.sv[0] + key % c.page_size * c.sv[1] + (int64_t)it.h * c.sv[2] + ch * 32;
-              const float vs = kQ8 ? c.vs[pg * c.svs[0] + key % c.page_size * c.svs[1] + (int64_t)it.h * c.svs[2]] : 1.f;
+        if (lost.nan | lost.up | lost.down) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float v = kQ8 ? ld(static_cast<const __nv_fp8_e4m3*>(c.v) + at + e) * vs
-                                    : ldf16(static_cast<const uint16_t*>(c.v) + at + e, kH);
-                if (!isfinite(v)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
-              }
-            }
+          for (int e = 0; e < 32; ++e) {
+            float v = __uint_as_float(o[e]);
+            if ((lost.up >> e) & 1u) v += INFINITY;
+            if ((lost.down >> e) & 1u) v -= INFINITY;
+            o[e] = (lost.nan >> e) & 1u ? 0x7fffffffu : __float_as_uint(v);
           }
         }
         if (valid && whole) {

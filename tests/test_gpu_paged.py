@@ -432,6 +432,47 @@ def test_non_finite_values_where_a_cta_walks_many_blocks(Hq, Hkv, cd):
     assert not torch.isfinite(o[~ok.cuda()][:, 70]).any()
 
 
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+def test_one_nan_behind_a_million_keys(cd):
+    """A row block that walks 2^20 keys by itself, with one NaN in the last
+    page: only the rows that see it are NaN, and no wait runs out meanwhile.
+    The cache is eight pages, each listed many times, and a last one. Beside
+    check's bounds, fp32 sums over 2^16 steps of 16 keys: 2^-8 relative to A,
+    and 2^-8 for the LSE."""
+    heads = torch.cuda.get_device_properties(0).multi_processor_count  # an item for every CTA
+    page, n, times, new = 128, 8, 1024, 40
+    lens, last = [n * times * page], n
+    cache, K, V = make_cache([(n + 1) * page], page, heads, 128, 128, DT[cd], seed=21, src=torch.bfloat16)
+    order = cache.block_table[0, :n + 1].clone()
+    cache.block_table = torch.cat([order[:n].repeat(times)[:-1], order[n:]])[None].contiguous()
+    cache.seq_lens.fill_(lens[0])
+    pg = int(order[last])
+    hit, see = page - 30, 10  # visible to the last 30 of the 40 new tokens
+    if cd == "e4m3":
+        cache.v.view(torch.uint8)[pg, hit, 1, 70] = 0x7F
+    else:
+        cache.v[pg, hit, 1, 70] = math.nan
+    q = seeded_q(new, heads, 128, torch.bfloat16, 22)
+    o, lse = run(q, cache, [new], allowed=eta.AllowedSet(causal=True), max_q=new)
+    assert torch.isnan(o[see:, 1, 70]).all()
+    for h in (0, 1, heads - 1):
+        k, v = K[0][:, h], V[0][:, h]
+        count = torch.full((n * page,), float(times), dtype=torch.float64)
+        count[-page:] -= 1  # its last listing is the last page
+        count = torch.cat([count, torch.ones(page, dtype=torch.float64)]).expand(new, -1).clone()
+        count[:, -page:] = (torch.arange(page) <= page - new + torch.arange(new)[:, None]).double()
+        x = q[:, h].double().cpu() @ k.T * 128 ** -0.5 + torch.log(count)
+        want_lse = torch.logsumexp(x, 1)
+        p = torch.exp(x - want_lse[:, None])
+        A = p @ v.abs()
+        ok = torch.ones(new, 128, dtype=torch.bool)
+        if h == 1:
+            ok[see:, 70] = False
+        err = (o[:, h].double().cpu() - p @ v).abs()
+        assert (err <= 2.0 ** -8 * (p @ v).abs() + (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -12) * A)[ok].all()
+        assert ((lse[:, h].double().cpu() - want_lse).abs() <= 2.0 ** -8).all()
+
+
 @pytest.mark.parametrize("new,kind", [(1, "decode"), (20, "chunk")])
 @pytest.mark.parametrize("cd", ["bf16", "e4m3"])
 def test_one_long_sequence_is_joined_from_many_shares(new, kind, cd):
