@@ -315,6 +315,23 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+def _on_stream(stream, make):
+    """make()'s new tensors (a tuple) for a call on `stream` (None: the current
+    one). They are allocated, and filled, on that stream, so that neither a
+    fill nor an earlier use of their memory is still at work when the call's
+    kernels run, and recorded for the current stream, on which the caller may
+    go on with them (and drop them)."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        made = make()
+    if here != stream:
+        for t in made:
+            t.record_stream(here)
+    return made
+
+
 def _is_topk(allowed: AllowedSet | None) -> bool:
     return allowed is not None and allowed.topk_idxs is not None
 
@@ -561,8 +578,10 @@ def attn_cache_read(cache: PagedCache, max_len: int | None = None, *, dtype=None
         elif dtype is None:
             dtype = torch.bfloat16 if cache.k.dtype == torch.float8_e4m3fn else cache.k.dtype
         B = cache.seq_lens.shape[0]
-        k = torch.zeros(B, H, T, d, dtype=dtype, device=device) if k is None else k
-        v = torch.zeros(B, H, T, cache.v.shape[3], dtype=dtype, device=device) if v is None else v
+        widths = ([d] if k is None else []) + ([cache.v.shape[3]] if v is None else [])
+        new = _on_stream(stream, lambda: [torch.zeros(B, H, T, w, dtype=dtype, device=device) for w in widths])
+        k = new[0] if k is None else k
+        v = new[-1] if v is None else v
     c = cache.packed()
     _check_on(device, k, v, workspace)
     rc = _on_device(device, load_library().attn_cache_read, stream, c, _packed(k), _packed(v),
@@ -591,9 +610,9 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = q.new_empty((rows, heads, cache.v.shape[3]))
+        out, = _on_stream(stream, lambda: (q.new_empty((rows, heads, cache.v.shape[3])),))
     if lse is None:
-        lse = q.new_empty((rows, heads), dtype=torch.float32)
+        lse, = _on_stream(stream, lambda: (q.new_empty((rows, heads), dtype=torch.float32),))
     m = allowed.to_c() if allowed else None
     cq, c, cu = _packed(q), cache.packed(), _cu_q_ptr(cu_q, cache)
     _check_on(device, cache.k, out, lse, workspace, *(allowed.tensors() if allowed else ()))
