@@ -358,14 +358,14 @@ def attn_fwd(q, k, v, allowed: AllowedSet | None = None, scale: float | None = N
     if scale is None:
         scale = q.shape[-1] ** -0.5
     if out is None:
-        out = q.new_empty((*q.shape[:-1], v.shape[-1]))
+        out, = _on_stream(stream, lambda: (q.new_empty((*q.shape[:-1], v.shape[-1])),))
     if lse is None:
-        lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
+        lse, = _on_stream(stream, lambda: (q.new_empty(q.shape[:-1], dtype=torch.float32),))
     m = allowed.to_c() if allowed else None
     cq, ck, cv, co, cl = (_packed(x) for x in (q, k, v, out, lse))
     need = lib.attn_fwd_workspace_size(cq, ck, cv, m)
     if workspace is None:
-        workspace = _workspace(need, q.device)
+        workspace, = _on_stream(stream, lambda: (_workspace(need, q.device),))
     _check_on(q.device, k, v, out, lse, workspace, *(allowed.tensors() if allowed else ()))
     rc = lib.attn_fwd(cq, ck, cv, m, scale, co, cl,
                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
@@ -383,19 +383,19 @@ def attn_bwd(q, k, v, o, do, lse, allowed: AllowedSet | None = None, scale: floa
         scale = q.shape[-1] ** -0.5
     topk = _is_topk(allowed)
     if dq is None:
-        dq = torch.empty_like(q)
+        dq, = _on_stream(stream, lambda: (torch.empty_like(q),))
     if dk is None:
-        dk = torch.empty_like(k)
+        dk, = _on_stream(stream, lambda: (torch.empty_like(k),))
     if dv is None and not topk:
-        dv = torch.empty_like(v)
+        dv, = _on_stream(stream, lambda: (torch.empty_like(v),))
     if dsink is None and allowed is not None and allowed.sink is not None:
-        dsink = torch.empty_like(allowed.sink, dtype=torch.float32)
+        dsink, = _on_stream(stream, lambda: (torch.empty_like(allowed.sink, dtype=torch.float32),))
     m = allowed.to_c() if allowed else None
     cq, ck, cv, co, cdo, cl = (_packed(x) for x in (q, k, v, o, do, lse))
     cdq, cdk, cdv = _packed(dq), _packed(dk), _packed(dv)
     need = lib.attn_bwd_workspace_size(cq, ck, cv, m)
     if workspace is None:
-        workspace = _workspace(need, q.device)
+        workspace, = _on_stream(stream, lambda: (_workspace(need, q.device),))
     _check_on(q.device, k, v, o, do, lse, dq, dk, dv, dsink, workspace,
               *(allowed.tensors() if allowed else ()))
     rc = lib.attn_bwd(cq, ck, cv, co, cdo, cl, m,

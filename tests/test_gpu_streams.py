@@ -67,3 +67,43 @@ def test_paged_attention(new):
     sizes = [q.numel() * 2, q.numel() // 128 * 4, eta.attn_paged_workspace_size(q, cache, a)]
     for x, y in zip(held_back(lambda s: eta.attn_paged_fwd(q, cache, cu, a, max_q=new, stream=s), *sizes), want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("sink", [False, True])
+def test_dense_forward_and_reverse(sink):
+    B, Hq, Hkv, T, d = 2, 8, 4, 600, 128
+    q, k, v, g = (seeded_q(B * h, T, d, torch.bfloat16, i).view(B, h, T, d) for i, h in enumerate((Hq, Hkv, Hkv, Hq)))
+    z = torch.randn(Hq, device="cuda") if sink else None
+    # (with lengths the forward's workspace holds a table that its kernel reads)
+    a = eta.AllowedSet(causal=True, lengths=torch.tensor([600, 333], dtype=torch.int32, device="cuda"), sink=z,
+                       deterministic=True)
+    o, lse = eta.attn_fwd(q, k, v, a)
+    want = eta.attn_bwd(q, k, v, o, g, lse, a)
+    sizes = [q.numel() * 2, lse.numel() * 4, eta.attn_fwd_workspace_size(q, k, v, a)]
+    for x, y in zip(held_back(lambda s: eta.attn_fwd(q, k, v, a, stream=s), *sizes), (o, lse)):
+        assert torch.equal(x, y)
+    sizes = [q.numel() * 2, k.numel() * 2, k.numel() * 2, eta.attn_bwd_workspace_size(q, k, v, a)]
+    got = held_back(lambda s: eta.attn_bwd(q, k, v, o, g, lse, a, stream=s), *sizes)
+    for x, y in zip(got[:3], want[:3]):
+        assert torch.equal(x, y)
+    assert sink == (got[3] is not None) and (not sink or torch.equal(got[3], want[3]))
+
+
+def test_a_dropped_workspace_is_not_taken_by_the_current_stream():
+    """The workspace that a call makes for itself goes back to its own stream's
+    memory: what the current stream allocates and fills next is not it."""
+    B, H, T, d = 1, 16, 2048, 128
+    q, k, v, g = (seeded_q(B * H, T, d, torch.bfloat16, i).view(B, H, T, d) for i in range(4))
+    a = eta.AllowedSet(causal=True, deterministic=True)
+    o, lse = eta.attn_fwd(q, k, v, a)
+    want = eta.attn_bwd(q, k, v, o, g, lse, a)
+    n = eta.attn_bwd_workspace_size(q, k, v, a)
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        torch.cuda.synchronize()
+        got = eta.attn_bwd(q, k, v, o, g, lse, a, stream=s)
+        for _ in range(4):
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x7F)
+        torch.cuda.synchronize()
+        for x, y in zip(got[:3], want[:3]):
+            assert torch.equal(x, y)
