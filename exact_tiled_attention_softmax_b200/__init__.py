@@ -203,7 +203,7 @@ class AllowedSet:
 
     block_mask: uint8 [nq_blocks, nk_blocks], or with leading [B, H] dims
     (size-1 dims broadcast). topk_idxs int32 [Tq, >= topk_max],
-    topk_length int32 [Tq], sink float32 [Hq]. lengths int32 [B] (active
+    topk_length int32 [Tq], sink float32 [Hq] (a shorter one is refused). lengths int32 [B] (active
     cells per batch row, Tq == Tk); starts int32 [B, Tq] or [Tq] (lowest
     allowed key of each query row, e.g. its packed segment's first cell).
     lse_kv_only / lse_neg_log2 select the LSE format that attn_fwd writes
@@ -336,6 +336,15 @@ def _is_topk(allowed: AllowedSet | None) -> bool:
     return allowed is not None and allowed.topk_idxs is not None
 
 
+def _mask_of(allowed: AllowedSet | None, q, dsink=None) -> AttnMaskC | None:
+    """The descriptor of a call on q, whose second dimension is its heads: the
+    kernels read a sink logit, and write a sink gradient, for each of them."""
+    for t, name in ((dsink, "dsink"), (allowed.sink if allowed else None, "sink")):
+        if t is not None and q.dim() > 1 and t.numel() < q.shape[1]:
+            raise ValueError(f"{name}: {t.numel()} entries for {q.shape[1]} query heads")
+    return allowed.to_c() if allowed else None
+
+
 def attn_fwd_workspace_size(q, k, v, allowed: AllowedSet | None = None) -> int:
     cq, ck, cv = _packed(q), _packed(k), _packed(v)
     m = allowed.to_c() if allowed else None
@@ -361,7 +370,7 @@ def attn_fwd(q, k, v, allowed: AllowedSet | None = None, scale: float | None = N
         out, = _on_stream(stream, lambda: (q.new_empty((*q.shape[:-1], v.shape[-1])),))
     if lse is None:
         lse, = _on_stream(stream, lambda: (q.new_empty(q.shape[:-1], dtype=torch.float32),))
-    m = allowed.to_c() if allowed else None
+    m = _mask_of(allowed, q)
     cq, ck, cv, co, cl = (_packed(x) for x in (q, k, v, out, lse))
     need = lib.attn_fwd_workspace_size(cq, ck, cv, m)
     if workspace is None:
@@ -390,7 +399,7 @@ def attn_bwd(q, k, v, o, do, lse, allowed: AllowedSet | None = None, scale: floa
         dv, = _on_stream(stream, lambda: (torch.empty_like(v),))
     if dsink is None and allowed is not None and allowed.sink is not None:
         dsink, = _on_stream(stream, lambda: (torch.empty_like(allowed.sink, dtype=torch.float32),))
-    m = allowed.to_c() if allowed else None
+    m = _mask_of(allowed, q, dsink)
     cq, ck, cv, co, cdo, cl = (_packed(x) for x in (q, k, v, o, do, lse))
     cdq, cdk, cdv = _packed(dq), _packed(dk), _packed(dv)
     need = lib.attn_bwd_workspace_size(cq, ck, cv, m)
@@ -416,7 +425,7 @@ def attn_bwd_noalloc(q, k, v, o, do, lse, allowed: AllowedSet | None = None, sca
     lib = load_library()
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    m = allowed.to_c() if allowed else None
+    m = _mask_of(allowed, q, dsink)
     cq, ck, cv, co, cdo, cl = (_packed(x) for x in (q, k, v, o, do, lse))
     cdq, cdk, cdv = _packed(dq), _packed(dk), _packed(dv)
     _check_on(q.device, k, v, o, do, lse, dq, dk, dv, dsink, *(allowed.tensors() if allowed else ()))
@@ -613,7 +622,7 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
         out, = _on_stream(stream, lambda: (q.new_empty((rows, heads, cache.v.shape[3])),))
     if lse is None:
         lse, = _on_stream(stream, lambda: (q.new_empty((rows, heads), dtype=torch.float32),))
-    m = allowed.to_c() if allowed else None
+    m = _mask_of(allowed, q)
     cq, c, cu = _packed(q), cache.packed(), _cu_q_ptr(cu_q, cache)
     _check_on(device, cache.k, out, lse, workspace, *(allowed.tensors() if allowed else ()))
 

@@ -175,6 +175,34 @@ def test_binding_refuses_host_tensors_and_wrong_tables():
         eta.PagedCache(pool, pool, table, lens[:1]).to_c()
 
 
+def test_binding_refuses_a_sink_shorter_than_the_heads():
+    """The library reads a logit, and writes a gradient, per query head; the
+    binding sees how many there are."""
+    torch = pytest.importorskip("torch")
+    z = torch.zeros(3)
+    a = eta.AllowedSet(causal=True, sink=z)
+    q, o, lse = torch.zeros(1, 4, 8, 16), torch.zeros(1, 4, 8, 16), torch.zeros(1, 4, 8)
+    with pytest.raises(ValueError, match="sink: 3 entries for 4"):
+        eta.attn_fwd(q, q, q, a)
+    with pytest.raises(ValueError, match="sink: 3 entries for 4"):
+        eta.attn_bwd(q, q, q, o, o, lse, a, dsink=torch.zeros(4))
+    full = eta.AllowedSet(causal=True, sink=torch.zeros(4))
+    with pytest.raises(ValueError, match="dsink: 3 entries for 4"):
+        eta.attn_bwd(q, q, q, o, o, lse, full, dsink=z)
+    with pytest.raises(ValueError, match="dsink: 3 entries for 4"):
+        eta.attn_bwd_noalloc(q, q, q, o, o, lse, full, dq=q, dk=q, dv=q, dsink=z)
+    topk = eta.AllowedSet(topk_idxs=torch.zeros(6, 2, dtype=torch.int32), sink=z)
+    with pytest.raises(ValueError, match="sink: 3 entries for 4"):
+        eta.attn_fwd(torch.zeros(6, 4, 16), torch.zeros(9, 16), torch.zeros(9, 16), topk)
+    pool = torch.zeros(4, 16, 2, 16)
+    cache = eta.PagedCache(pool, pool, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="sink: 3 entries for 4"):
+        eta.attn_paged_fwd(torch.zeros(6, 4, 16), cache, None, a)
+    # one that is long enough goes on to the next check
+    with pytest.raises(ValueError, match="CUDA"):
+        eta.attn_paged_fwd(torch.zeros(6, 4, 16), cache, None, full)
+
+
 def test_quartic_exponential():
     """The quartic that stands in for some exponentials where the sum's logarithm
     is an fp32 output: the kernel's fp32 steps in NumPy, and its coefficients
