@@ -733,6 +733,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     const int boxes = kPTile / box;
     int n = 0;
+    [[maybe_unused]] int nk8 = 0;  // e4m3: raw K tiles under way or landed (n: K and V)
     bool ok = true;
     while (ok && pieces.next(p, pl, it, k0, k1, u)) {
       hv.init(p, it);
@@ -783,6 +784,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           }
           __syncwarp();
           if (lane < boxes) tma_load_4d(sbase + kPRaw + lane * box * 128, &tk, kf, 0, off, it.h, page);
+          ++nk8;
           ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl->raw_empty[1]), (n & 1) ^ 1, abort_flag, status));
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(vf, kPRawB);
@@ -803,9 +805,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         wait_bar(smem_u32(&ctl->k_full[r % kPStages]), (r / kPStages) & 1, &calm, nullptr);
         wait_bar(smem_u32(&ctl->v_full[r % kPStages]), (r / kPStages) & 1, &calm, nullptr);
       }
-    } else if (n > 0) {
-      wait_bar(smem_u32(&ctl->raw_full[0]), (n - 1) & 1, &calm, nullptr);
-      wait_bar(smem_u32(&ctl->raw_full[1]), (n - 1) & 1, &calm, nullptr);
+    } else {
+      // (an abort between the two leaves a tile's K under way without its V)
+      if (nk8 > 0) wait_bar(smem_u32(&ctl->raw_full[0]), (nk8 - 1) & 1, &calm, nullptr);
+      if (n > 0) wait_bar(smem_u32(&ctl->raw_full[1]), (n - 1) & 1, &calm, nullptr);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (whole warp; one elected lane issues)
