@@ -568,7 +568,7 @@ __device__ __forceinline__ float softmax_scaled_tile(uint32_t tS, const float* k
       } else {
         y01 = f2_pack(ex2(x[0]), ex2(x[1]));
         // every fourth pair on the FMA pipe, as in the 16-bit rows
-        y23 = (e & 4) ? exp2_pair<true>(fmaxf(x[2], -125.f), fmaxf(x[3], -125.f)) : f2_pack(ex2(x[2]), ex2(x[3]));
+        y23 = (e & 4) ? exp2_pair<true>(x[2], x[3]) : f2_pack(ex2(x[2]), ex2(x[3]));
         f2_unpack(y01, x[0], x[1]);
         f2_unpack(y23, x[2], x[3]);
       }

@@ -46,9 +46,13 @@ __device__ __forceinline__ float move_max(float mx, float& m_run) {
   return alpha;
 }
 
+// 2^x of two by a polynomial: x below -125 counts as that or, with kFine, below
+// -127 as minus infinity: at -127 the polynomial is 1 and its exponent field
+// becomes 0, so the result is 0 (between the two it is below 2^-125).
 template <bool kFine>
 __device__ __forceinline__ uint64_t exp2_pair(float x0, float x1) {
-  return kFine ? exp2_fma2_fine(f2_pack(x0, x1)) : exp2_fma2(f2_pack(x0, x1));
+  return kFine ? exp2_fma2_fine(f2_pack(fmaxf(x0, -127.f), fmaxf(x1, -127.f)))
+               : exp2_fma2(f2_pack(fmaxf(x0, -125.f), fmaxf(x1, -125.f)));
 }
 
 // One S row (128 keys, all allowed, no dropout) of the calling thread's TMEM
@@ -110,7 +114,7 @@ __device__ __forceinline__ float softmax_full_tile(uint32_t tS, float scale_log2
       float x0, x1;
       f2_unpack(x, x0, x1);
       const uint64_t pp = poly_pair<kDrop>(e)
-                              ? exp2_pair<kStrict>(fmaxf(x0, -125.f), fmaxf(x1, -125.f))
+                              ? exp2_pair<kStrict>(x0, x1)
                               : f2_pack(ex2(x0), ex2(x1));
       if (e & 1)
         acc1 = f2_add(acc1, pp);

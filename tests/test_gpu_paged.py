@@ -544,6 +544,38 @@ def test_nan_scores_make_the_row_nan():
         assert torch.isfinite(o[1:]).all() and torch.isfinite(lse[1:]).all()
 
 
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("cd", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("kind,new", [("decode", 1), ("few", 4), ("chunk", 150), ("any", 4)])
+def test_rows_whose_scores_are_all_minus_infinity(kind, new, cd, sink):
+    """They count as empty, over tiles that are seen whole and in part alike;
+    those of the other sequence and the other K/V head keep their results."""
+    page = 7 if kind == "any" else 16
+    lens, head = [600, 290], 1
+    qd = torch.float16 if cd == "f16" else torch.bfloat16
+    cache, K, V = make_cache(lens, page, 2, 128, 128, DT[cd], seed=23, src=qd)
+    pos = torch.arange(lens[0])
+    at = cache.block_table[0].long().cpu()[pos // page].cuda(), (pos % page).cuda()
+    if cd == "e4m3":  # every score is negative and its scale infinite
+        row = torch.zeros(128)
+        row[0] = -1
+        cache.k.view(torch.uint8)[at[0], at[1], head] = row.to(E4M3).view(torch.uint8).cuda()
+        cache.k_scale[at[0], at[1], head] = math.inf
+    else:
+        cache.k[at[0], at[1], head, 0] = -math.inf
+    q = seeded_q(2 * new, 4, 128, qd, 24)
+    q[..., 0] = 1
+    z = torch.randn(4, device="cuda") if sink else None
+    o, lse = run(q, cache, [new, new], allowed=eta.AllowedSet(causal=True, sink=z), max_q=new)
+    assert (o[:new, 2:] == 0).all()
+    empty = torch.full((2,), -math.inf) if z is None else z[2:].cpu()
+    assert torch.allclose(lse[:new, 2:].cpu(), empty.expand(new, 2), rtol=2.0 ** -22, atol=0)
+    ref = reference(q, K, V, [new, new], lens, 128 ** -0.5, sink=None if z is None else z.cpu())
+    ok = torch.ones(2 * new, 4, dtype=torch.bool)
+    ok[:new, 2:] = False
+    check(o[ok.cuda()], lse[ok.cuda()], *[r[ok] for r in ref], tensor_core=True, cache=cd)
+
+
 @pytest.mark.parametrize("kind,new", [("decode", 1), ("chunk", 140)])
 def test_scores_of_large_spread(kind, new):
     """Scores that grow along the keys move the running maximum in every tile;

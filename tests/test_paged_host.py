@@ -251,3 +251,23 @@ def test_more_sequences_than_positions_are_refused(lib):  # noqa: F811
     c = _cache(batch=(1 << 30) + 1)
     assert _write(lib, c) == eta.ATTN_ERR_UNSUPPORTED
     assert _fwd(lib, c) == eta.ATTN_ERR_UNSUPPORTED
+
+
+def test_quartic_exponential_at_its_lower_end():
+    """The kernels clamp its argument at -127, where it is exactly 0, so that a
+    score of -inf has no share; above that it is small and not negative."""
+    import numpy as np
+    f32 = np.float32
+    c = [f32(x) for x in (1.0, 0.6931219696998596, 0.24023719131946564, 0.05591689422726631, 0.00960039533674717)]
+    text = open(os.path.join(ROOT, "exact_tiled_attention_softmax_b200", "csrc", "sm100_ptx.cuh")).read()
+    assert all(f"{float(x)!r}f" in text for x in c[1:])
+    x = np.concatenate([[f32(-127)], np.linspace(-127, -124, 100_001, dtype=f32)])
+    t = (x + f32(12582912.0)).astype(f32)
+    f = (x - (t - f32(12582912.0))).astype(f32)
+    p = np.full_like(f, c[4])
+    for a in c[3::-1]:
+        p = (p * f + a).astype(f32)
+    n = t.view(np.int32) - np.int32(0x4B400000)
+    got = (p.view(np.int32) + (n << 23)).view(f32)
+    assert got[0] == 0 and not np.signbit(got[0])
+    assert (got >= 0).all() and (got[x <= -125] <= f32(2.0) ** -124).all()
