@@ -1238,6 +1238,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       for (int ch = 0; ch < 4; ++ch) {
         LostColumns lost{0u, 0u, 0u};
         if (lost0 >= 0) lost = lost_columns<kH, kQ8>(p, it, hv, lost0, lost1, pos, valid, box, ch);
+        if (whole && l_run == 0.f) lost = LostColumns{0u, 0u, 0u};  // an empty row (a part's: the join knows)
         uint32_t o[32];
         if (got > 0) {
           tmem_ld32(tO + ch * 32, o);

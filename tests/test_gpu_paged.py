@@ -544,6 +544,32 @@ def test_nan_scores_make_the_row_nan():
         assert torch.isfinite(o[1:]).all() and torch.isfinite(lse[1:]).all()
 
 
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind,new,L,B", [("decode", 1, 300, 1), ("few", 4, 300, 1), ("any", 4, 300, 1),
+                                          ("shares", 150, 3000, 1), ("whole", 40, 200, 300)])
+def test_empty_rows_stay_empty_over_values_that_are_not_finite(kind, new, L, B, cd):
+    """Scores of -inf throughout, and NaN in values of the last, partly visible
+    tile: the rows are 0 and -inf, whether one CTA walks a row block or several."""
+    page = 7 if kind == "any" else 16
+    cache, _, _ = make_cache([L], page, 1, 128, 128, DT[cd], seed=25, src=torch.bfloat16)
+    pos = torch.arange(L)
+    cache.block_table, cache.seq_lens = cache.block_table.repeat(B, 1), cache.seq_lens.repeat(B)
+    at = cache.block_table[0].long().cpu()[pos // page].cuda(), (pos % page).cuda()
+    if cd == "e4m3":
+        row = torch.zeros(128)
+        row[0] = -1
+        cache.k.view(torch.uint8)[at[0], at[1]] = row.to(E4M3).view(torch.uint8).cuda()
+        cache.k_scale[at] = math.inf
+        cache.v.view(torch.uint8)[at[0][-2], at[1][-2], 0, 70] = 0x7F
+    else:
+        cache.k[at[0], at[1], :, 0] = -math.inf
+        cache.v[at[0][-2], at[1][-2], 0, 70] = math.nan
+    q = seeded_q(B * new, 4, 128, torch.bfloat16, 26)
+    q[..., 0] = 1
+    o, lse = run(q, cache, [new] * B, allowed=eta.AllowedSet(causal=True), max_q=new)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
 @pytest.mark.parametrize("sink", [False, True])
 @pytest.mark.parametrize("cd", ["bf16", "f16", "e4m3"])
 @pytest.mark.parametrize("kind,new", [("decode", 1), ("few", 4), ("chunk", 150), ("any", 4)])
