@@ -677,9 +677,11 @@ attn_status attn_cache_read(const attn_cache* cache, attn_tensor* k, attn_tensor
   if ((int64_t)p.batch * p.Hkv >= kMaxRowWarps / (T ? T : 1)) return ATTN_ERR_UNSUPPORTED;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if ((st = optional_status(workspace, workspace_bytes, cs, p)) != ATTN_OK) return st;
-  if (!p.batch || !T) return ATTN_OK;
+  // Rows past what the table can hold are never written: at most 2^30 of them are looked at.
+  const int64_t cap = (int64_t)p.max_pages * p.page_size, rows = T < cap ? T : cap;
+  if (!p.batch || !rows) return ATTN_OK;
   const int64_t sok[3] = {k->stride[0], k->stride[1], k->stride[2]}, sov[3] = {v->stride[0], v->stride[1], v->stride[2]};
-  return cuda_status(launch_cache_read(p, k->data, sok, v->data, sov, (int)T, k->dtype, cs));
+  return cuda_status(launch_cache_read(p, k->data, sok, v->data, sov, (int)rows, k->dtype, cs));
 }
 
 size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, const attn_mask* mask) {

@@ -534,6 +534,23 @@ def test_read_into_one_given_tensor():
     assert torch.equal(got_v[0, :, :33].transpose(0, 1).double().cpu(), V[0]) and (got_v[0, :, 33:] == 0).all()
 
 
+def test_read_into_as_many_rows_as_a_tensor_can_have():
+    """2^31 - 1 rows a head, of which the table holds 48."""
+    cache, K, _ = make_cache([33], 16, 1, 8, 8, torch.bfloat16)
+    cache.v = cache.k
+    T = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 34 GB of device memory")
+    x = torch.empty(1, 1, T, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, :, :64] = 7
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    eta.attn_cache_read(cache, k=x, v=x, workspace=ws)
+    assert eta.attn_get_status(ws) == 0
+    assert torch.equal(x[0, 0, :33].double().cpu(), K[0][:, 0]) and (x[0, 0, 33:64] == 7).all()
+    del x
+    torch.cuda.empty_cache()
+
+
 def test_nan_scores_make_the_row_nan():
     for new, page in ((1, 16), (150, 16), (2, 7)):
         cache, _, _ = make_cache([300], page, 2, 128, 128, torch.bfloat16)
