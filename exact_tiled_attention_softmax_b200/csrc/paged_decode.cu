@@ -49,6 +49,7 @@ constexpr int kDTile = kDWarps * kPiece;
 constexpr float kLog2eD = 1.4426950408889634f;
 constexpr int kMinTiles = 2;      // key tiles a CTA takes at least
 constexpr float kRescaleD = 8.f;  // move the running maximum only past 2^8
+constexpr float kScaleDown = 0x1p-30f, kScaleUp = 0x1p30f;  // e4m3, on V's scales
 
 enum { kBf16 = 0, kF16 = 1, kE4m3Bf16 = 2, kE4m3F16 = 3 };  // cache type (and query type)
 
@@ -376,16 +377,19 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
         }
         // ---- scale, mask, running summary. Element e: key j0 + g8 + 8 (e >> 1),
         // row 8 nt + 2 t4 + (e & 1).
-        // The running reference m of an e4m3 row is that of s + log2(V's scale),
-        // so that the operand 2^(s - m) scale stays within 2^8 of its
-        // largest value whatever the scales are; the sum takes 2^(s - m)
-        // itself, in fp32. (A scale below 2^-60 counts as 2^-60 there.)
+        // The running reference m of an e4m3 row is that of s + log2(v), v being
+        // 2^-30 times V's scale, so that the operand 2^(s - m) v stays within 2^8
+        // of its largest value whatever the scales are; the sum takes 2^(s - m)
+        // itself, in fp32. (v below 2^-90 counts as that there. With the 2^-30 the
+        // sum's largest term is between 2^-90 and 2^98 for scales from 2^-60 to
+        // 2^120, so that terms 2^36 times smaller still count.)
         float ksc[2] = {1.f, 1.f}, vsc[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
         if constexpr (kQ8) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             lds64(st + 2 * R::kTileB + (g8 + 8 * i) * 8, ksc[i], vsc[i]);
-            lv[i] = fminf(fmaxf(__log2f(fabsf(vsc[i])), -60.f), 120.f);
+            vsc[i] *= kScaleDown;
+            lv[i] = fminf(fmaxf(__log2f(fabsf(vsc[i])), -90.f), 90.f);
           }
         }
 #pragma unroll
@@ -573,7 +577,8 @@ __global__ void __launch_bounds__(kDThreads, (Ring<kMode, kNT>::kCtas)) paged_de
         for (int j = 0; j < 8; ++j)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            wo[r * kDD + (kQ8 ? 16 * g8 + 2 * j + i : 16 * j + 8 * i + g8)] = acc[nt][j][2 * i + e];
+            wo[r * kDD + (kQ8 ? 16 * g8 + 2 * j + i : 16 * j + 8 * i + g8)] =
+                kQ8 ? acc[nt][j][2 * i + e] * kScaleUp : acc[nt][j][2 * i + e];
         if (g8 == 0) {
           wm[r] = m[nt][e];
           wm[kRows + r] = l[nt][e];

@@ -351,6 +351,8 @@ size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, 
  * ATTN_E4M3 cache: times the value row's scale where max_q asks for the
  * few-token kernel; the other one takes value rows as fp16(code * scale / 2^e)
  * with one power of two per 32 keys, which multiplies their probabilities.
+ * Where the value scales that a row sees differ by more than a factor of
+ * 2^100, the keys of the smallest may drop out of its sum.
  * Infinities and NaN in rows a query does not see
  * do not reach it. A row whose allowed scores are all -inf counts as empty.
  * max_q: the largest n_b, if the caller knows it, else 0: it chooses

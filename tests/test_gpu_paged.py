@@ -509,6 +509,31 @@ def test_e4m3_with_other_score_factors(kind, scale):
     check(o, lse, o_ref, l_ref, A + top * 2.0 ** 9, tensor_core=True, cache=E4M3)
 
 
+@pytest.mark.parametrize("other", [2.0 ** 20, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("kind,new", [("decode", 1), ("few", 4), ("chunk", 150), ("any", 4)])
+def test_one_value_row_of_the_largest_scale(kind, new, other):
+    """A value row near the end of fp32's range takes part of the probability,
+    several hundred rows of scales within 2^100 of its own the rest: none of
+    their shares is lost from the sum, though 2^(score - reference) is tiny."""
+    page, L, big = 7 if kind == "any" else 16, 700, 333
+    cache, K, V = make_cache([L], page, 1, 128, 128, E4M3, seed=27, src=torch.bfloat16)
+    pos = torch.arange(L)
+    at = cache.block_table[0].long().cpu()[pos // page].cuda(), (pos % page).cuda()
+    k = torch.zeros(L, 1, 128)
+    k[big, 0, 0] = 1
+    cache.k.view(torch.uint8)[at[0], at[1]] = k.to(E4M3).view(torch.uint8).cuda()
+    cache.k_scale[at] = 1.0
+    V[0] = V[0] / cache.v_scale[at].double().cpu()[..., None]  # the codes
+    scales = torch.full((L, 1), other)
+    scales[big] = 2.0 ** 118
+    cache.v_scale[at] = scales.cuda()
+    q = torch.zeros(new, 4, 128, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 9  # 2^9 times another key's share, of which there are 2^9.4
+    o, lse = run(q, cache, [new], allowed=eta.AllowedSet(causal=True), scale=math.log(2), max_q=new)
+    K, V = [k.double()], [V[0] * scales.double()[..., None]]
+    check(o, lse, *reference(q, K, V, [new], [L], math.log(2)), tensor_core=True, cache=E4M3)
+
+
 @pytest.mark.parametrize("cd", ["bf16", "e4m3"])
 @pytest.mark.parametrize("kind", ["decode", "chunk"])
 def test_unaligned_tensors(kind, cd):
