@@ -432,6 +432,21 @@ def test_non_finite_values_where_a_cta_walks_many_blocks(Hq, Hkv, cd):
     assert not torch.isfinite(o[~ok.cuda()][:, 70]).any()
 
 
+@pytest.mark.parametrize("kind,most", [("decode", 1), ("chunk", 40)])
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+def test_thousands_of_sequences(kind, most, cd):
+    """More sequences than a block has threads and than the plan's lists in
+    shared memory hold; every fifth brings no token."""
+    g = torch.Generator().manual_seed(30)
+    B = 2500
+    new = [0 if b % 5 == 3 else int(x) for b, x in enumerate(torch.randint(1, most + 1, (B,), generator=g))]
+    lens = [n + int(x) for n, x in zip(new, torch.randint(1, 70, (B,), generator=g))]
+    cache, K, V = make_cache(lens, 16, 1, 128, 128, DT[cd], seed=31, src=torch.bfloat16)
+    q = seeded_q(sum(new), 2, 128, torch.bfloat16, 32)
+    o, lse = run(q, cache, new, allowed=eta.AllowedSet(causal=True), max_q=most)
+    check(o, lse, *causal_reference(q, K, V, new, lens, 128 ** -0.5), tensor_core=True, cache=cd)
+
+
 @pytest.mark.parametrize("cd", ["bf16", "e4m3"])
 def test_one_nan_behind_a_million_keys(cd):
     """A row block that walks 2^20 keys by itself, with one NaN in the last
