@@ -612,7 +612,10 @@ def attn_paged_fwd(q, cache: PagedCache, cu_q=None, allowed: AllowedSet | None =
     holds them: query i of a sequence's n new tokens sits at position
     seq_len - n + i. allowed: causal, window_left, window_first, sink and the
     LSE formats. max_q: the largest number of new tokens of a sequence, when
-    known (it only chooses between kernels). Returns (o [rows, Hq, dv], lse
+    known. It only chooses between kernels, but matters for speed: left out
+    with cu_q, all rows count as one sequence's, and a batch of single tokens
+    takes the kernel for long chunks (64 sequences of 8192 keys: 461 us
+    instead of 325 in bf16, 667 instead of 206 in e4m3). Returns (o [rows, Hq, dv], lse
     [rows, Hq])."""
     lib, device = load_library(), q.device
     rows, heads, d = q.shape

@@ -11,8 +11,10 @@
 // 16-byte pieces, K and V in the same launch. With a full division per
 // element the write of an 8192-token prompt was bound by instructions.
 // Measured on the device (8 heads of 128): the new tokens of 64 bf16 sequences
-// 3.0 us (a launch), a bf16 prompt of 8192 tokens into e4m3 15.1-15.6 us
-// (3.3 TB/s; 61 % of the issue slots, the quotients' chains bound it), eight
+// 3.0 us (a launch), a bf16 prompt of 8192 tokens as it is 13.9 us with its
+// rows in HBM (4.8 TB/s, 0.74 of the measured copy rate; one round of loads and
+// stores per warp) and 8.6 us with them in L2, into e4m3 17.4 and 15.1-15.8 us
+// (3.2 TB/s; 62 % of the issue slots, the quotients' chains bound it), eight
 // ragged e4m3 sequences of up to 4096 read back as bf16 27.4 us (5.5 TB/s, 0.84
 // of the measured copy rate), 1000 fp16 positions read back 3.2 us.
 #include <math.h>

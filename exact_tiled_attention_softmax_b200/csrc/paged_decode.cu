@@ -21,10 +21,10 @@
 // in the CTAs' order, so the result does not depend on timing.
 //
 // Measured on the device, joins included (32 query heads over 8): 64 e4m3
-// sequences of up to 8192 keys 153 us = 5.1 TB/s of cache (0.77 of the measured
+// sequences of up to 8192 keys 151 us = 5.1 TB/s of cache (0.78 of the measured
 // copy rate; no unit is full, the warps wait on fixed instruction latencies
 // and at 166 registers 12 of them share an SM), 32 fp16 sequences of up to
-// 16384 with a window of 1024 and four first keys 34.8 us = 3.9 TB/s (an item
+// 16384 with a window of 1024 and four first keys 34.6 us = 3.9 TB/s (an item
 // is 17 tiles, so starting and joining shows), one sequence of 2000 bf16 keys
 // 11.2 us (two launches and their latencies; its bytes are 1.3 us).
 #include <math.h>
@@ -65,6 +65,8 @@ struct Ring {
   // 64 e4m3 sequences of up to 8192 keys took 159 us with 3 CTAs of 4 stages,
   // 164 with 4 of 3, 184 with 4 of 2, 190 with 2 of 5; the fp16 window workload
   // of 32 sequences 35.1 us with 2 of 3, 36.6 with 3 of 2, 51 with 2 of 4.
+  // (Tuned on 8 rows: with 16 rows of an e4m3 cache three CTAs leave 168
+  // registers, and 100 to 176 bytes spill; two CTAs are untried there.)
   static constexpr int kCtas = kQ8 ? 3 : 2;
   static constexpr int kWarpB = kStages * kStageB;
   static constexpr int kSmem = kDWarps * kWarpB;
@@ -631,9 +633,9 @@ cudaError_t launch_mode(const PagedP& p, SplitP sp, cudaStream_t st) {
 
 // Blocks of 8 or 16 rows. A 16-bit cache is bound by its bytes either way (64
 // sequences of 8192 keys: 317 us with 8 rows and with 16); an e4m3 one by
-// instructions, 200 against 310 us, so that three blocks of 8 take less than two
-// of 16 (20 rows: 572 against 626 us) and two of 8 more than one of 16 (12 rows:
-// 386 against 323 us).
+// instructions, 206 us with 8 rows against 320 with 16 (whose form also spills,
+// see Ring), so that three blocks of 8 take less than two of 16 (20 rows: 574
+// against 626 us) and two of 8 more than one of 16 (12 rows: 386 against 318 us).
 template <int kMode>
 cudaError_t launch_rows(const PagedP& p, int rows, const SplitP& sp, cudaStream_t st) {
   const bool eights = rows <= 8 || (kMode >= kE4m3Bf16 && rows > 16 && rows <= 24);

@@ -19,7 +19,9 @@
 // In tiles that some row sees only in part, or that hold such a box, the
 // checker warps (e4m3: the converting ones) therefore take non-finite elements
 // of V out of the operand; rows that do see such a key get them back in the
-// epilogue, where the result is not finite whatever the probability was.
+// epilogue, where the result is not finite whatever the probability was (but a
+// row whose scores are all -inf stays empty). 43 us more for the blocks of one
+// tile that lost some.
 //
 // Work split: plan_kernel lists the blocks of every sequence, deals whole items
 // (block, K/V head) to the CTAs round by round, so that the CTAs walk the same
@@ -29,12 +31,14 @@
 // in the CTAs' order, so the result does not depend on timing.
 //
 // Measured on the device, plan and joins included (32 query heads over 8): 2048
-// new tokens at the end of 16384 keys, bf16 480 us = 1073 TFLOP/s (0.65 of the
-// measured cuBLAS rate: the two halves' softmax chains and the tensor pipe, 52 %
-// busy, alternate), e4m3 0.71-0.74 ms = 700-725 TFLOP/s (the K scales' loads in
-// the softmax warps and the conversion come on top, and 512 threads leave 128
-// registers); eight sequences of 1 to 256 new tokens over up to 4096 bf16 keys
-// 118-120 us = 520 TFLOP/s, of which the plan and the joins are about 15.
+// new tokens at the end of 16384 keys, bf16 483-490 us = 1060 TFLOP/s in short
+// bursts at 1965 MHz (0.64 of the measured cuBLAS rate: the two halves' softmax
+// chains and the tensor pipe, 50 % busy, alternate) and 547 us under load that
+// meets the power cap (1.72 GHz); e4m3 0.69-0.72 ms = 720-750 TFLOP/s (the K
+// scales' loads in the softmax warps and the conversion come on top; 512 threads
+// leave 128 registers, of which the softmax spills 53 words and warps 2 and 3
+// use none); eight sequences of 1 to 256 new tokens over up to 4096 bf16 keys
+// 119 us = 520 TFLOP/s, of which the plan and the joins are about 15.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>

@@ -237,7 +237,10 @@ attn_status attn_fwd(const attn_tensor* q, const attn_tensor* k,
  * deterministic (bitwise identical across runs); the dense dq and the
  * tensor-core top-k dKV are summed with floating-point atomics and are
  * not, unless mask->bwd_flags holds ATTN_BWD_DETERMINISTIC (then every
- * output is). */
+ * output is; the dense dq is as well where dsink and first keys meet, whose
+ * sum over 16-bit rows takes delta in fp32 from a pass of its own. Without
+ * first keys dsink takes delta from the stored 16-bit o and is off by about
+ * 1e-3 of its terms). */
 attn_status attn_bwd(const attn_tensor* q, const attn_tensor* k,
                      const attn_tensor* v, const attn_tensor* o,
                      const attn_tensor* do_, const attn_tensor* lse,
@@ -356,7 +359,9 @@ size_t attn_paged_workspace_size(const attn_tensor* q, const attn_cache* cache, 
  * Infinities and NaN in rows a query does not see
  * do not reach it. A row whose allowed scores are all -inf counts as empty.
  * max_q: the largest n_b, if the caller knows it, else 0: it chooses
- * between kernels and never changes which tokens are attended. The result is
+ * between kernels and never changes which tokens are attended. With 0 and a
+ * cu_q all rows count as one sequence's, which takes the kernel for long
+ * chunks: for batches of single tokens 1.4 to 3 times slower. The result is
  * bitwise reproducible for the same arguments on the same device. */
 attn_status attn_paged_fwd(const attn_tensor* q, const int32_t* cu_q, const attn_cache* cache,
                            const attn_mask* mask, float scale, int32_t max_q, attn_tensor* o, attn_tensor* lse,
