@@ -51,8 +51,9 @@ enum : uint8_t { kEmpty = 0, kFull = 1, kPartial = 2 };
 // + qoff). Row i allows [max(c0, i-W+1), min(c1, i)], so some row qualifies
 // iff i can be chosen with c0 <= i (causal) and i <= c1 + W - 1 (window). The
 // window does not apply to columns below m.first (0 when not set; kFirst false
-// here and below: known to be 0, which the query-centric dQ pass uses: its
-// issuer walks the tiles between products, and the tests cost it 2 %).
+// here and below: known to be 0, which the query-centric dQ pass and the
+// forward kernel use: the issuer of the one walks the tiles between products,
+// and the tests cost it 2 %; those of the other cost its dropout form 1.6 %).
 template <bool kFirst = true>
 __device__ __forceinline__ void band_test(const MaskP& m, int64_t r0, int64_t r1, int64_t c0, int64_t c1, bool& any,
                                           bool& all) {
@@ -215,6 +216,7 @@ struct FwdCtl {
 };
 
 // Key-tile range that can hold allowed keys for rows [q0, q0 + rows).
+template <bool kFirst>
 __device__ __forceinline__ void fwd_key_tiles(const MaskP& m, int b, int Tq, int Tk, int q0, int rows, int& lo,
                                               int& hi) {
   const int nkt = (Tk + kBN - 1) / kBN;
@@ -229,7 +231,7 @@ __device__ __forceinline__ void fwd_key_tiles(const MaskP& m, int b, int Tq, int
   }
   if (m.flags & ATTN_MASK_WINDOW) {
     const int64_t first = (int64_t)q0 + m.qoff - m.window + 1;
-    lo = first > 0 && !m.first ? (int)(first / kBN) : 0;  // with first keys: FwdGap
+    lo = first > 0 && !(kFirst && m.first) ? (int)(first / kBN) : 0;  // with first keys: FwdGap
   }
   if (m.lengths) {  // Tq = Tk here
     const int64_t L = active_len(m, b, Tk);
@@ -266,11 +268,13 @@ __device__ __forceinline__ uint8_t wg_class(const FwdArgs& a, int b, int h, int 
 // First key tile after `from` (up to kt_hi) with allowed keys for either
 // query tile of the CTA (qt0, qt0 + 1); kt_hi + 1 when none. flags: bit w
 // set when query tile qt0 + w has allowed keys there.
+template <bool kFirst>
 __device__ __forceinline__ int fwd_next_tile(const FwdArgs& a, int b, int h, int qt0, const FwdGap& gap, int kt_hi,
                                              int from, uint32_t& flags) {
   for (int kt = from + 1; kt <= kt_hi; ++kt) {
-    if (kt == gap.lo && (kt = gap.hi) > kt_hi) break;
-    flags = (wg_class(a, b, h, qt0, kt) != kEmpty ? 1u : 0u) | (wg_class(a, b, h, qt0 + 1, kt) != kEmpty ? 2u : 0u);
+    if (kFirst && kt == gap.lo && (kt = gap.hi) > kt_hi) break;
+    flags = (wg_class<kFirst>(a, b, h, qt0, kt) != kEmpty ? 1u : 0u) |
+            (wg_class<kFirst>(a, b, h, qt0 + 1, kt) != kEmpty ? 2u : 0u);
     if (flags) return kt;
   }
   flags = 0;
@@ -304,6 +308,7 @@ __device__ __noinline__ KeyInterval clip_row_keys(const int32_t* lengths, const 
 // (bit c <-> key j0 + c). The causal/window conditions give one interval;
 // a block mask that is constant over (64-row slice, 128-key tile) blocks is
 // already folded into the tile class, otherwise it is looked up per key.
+template <bool kFirst>
 __device__ __forceinline__ void fwd_row_bits(const FwdArgs& a, int b, int h, int64_t i, int64_t j0, uint8_t slice_cls,
                                              uint64_t& w0, uint64_t& w1) {
   w0 = w1 = 0ull;
@@ -318,10 +323,10 @@ __device__ __forceinline__ void fwd_row_bits(const FwdArgs& a, int b, int h, int
     lo = iv.lo;
     hi = iv.hi;
   }
-  if (lo > hi && !a.m.first) return;
+  if (lo > hi && !(kFirst && a.m.first)) return;
   w0 = range_bits64(lo - j0, hi - j0);
   w1 = range_bits64(lo - j0 - 64, hi - j0 - 64);
-  if (j0 < a.m.first) {  // the tile's first keys, which the window does not bound
+  if (kFirst && j0 < a.m.first) {  // the tile's first keys, which the window does not bound
     const int64_t fh = a.m.first - 1 < hi ? a.m.first - 1 : hi;
     w0 |= range_bits64(0, fh - j0);
     w1 |= range_bits64(-64, fh - j0 - 64);
@@ -432,8 +437,9 @@ __device__ __forceinline__ float softmax_full_tile_drop(uint32_t tS, float scale
 // into the warpgroup's own S columns of TMEM and read from there by the PV
 // MMA; S of the next tile lands in the same columns only after that PV, in
 // issue order.
-// kFirst (a window with first keys): exponentials accurate to 3e-6, since that
-// form's sink gradient is carried to fp32 accuracy through the LSE.
+// kFirst (a window with first keys): without dropout exponentials accurate to
+// 3e-6, since that form's sink gradient is carried to fp32 accuracy through the
+// LSE (with dropout every exponential is the hardware's anyway).
 template <bool kH, bool kDrop, bool kFirst>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -462,8 +468,8 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
   const int q0 = ct * kFwdRows;
   const int qt0 = 2 * ct;
   int kt_lo, kt_hi;
-  fwd_key_tiles(a.m, b, a.Tq, a.Tk, q0, kFwdRows, kt_lo, kt_hi);
-  const FwdGap gap = fwd_gap(a.m, q0);
+  fwd_key_tiles<kFirst>(a.m, b, a.Tq, a.Tk, q0, kFwdRows, kt_lo, kt_hi);
+  const FwdGap gap = kFirst ? fwd_gap(a.m, q0) : FwdGap{-1, -1};
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ctl->q_full), 1);
@@ -506,9 +512,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
     // issuer, which reads each stage's flags from tinfo.
     int n = 0;
     uint32_t fl;
-    for (int kt = fwd_next_tile(a, b, h, qt0, gap, kt_hi, kt_lo - 1, fl); kt <= kt_hi;) {
+    for (int kt = fwd_next_tile<kFirst>(a, b, h, qt0, gap, kt_hi, kt_lo - 1, fl); kt <= kt_hi;) {
       uint32_t nfl;
-      const int nk = fwd_next_tile(a, b, h, qt0, gap, kt_hi, kt, nfl);
+      const int nk = fwd_next_tile<kFirst>(a, b, h, qt0, gap, kt_hi, kt, nfl);
       const int s = n % kStages;
       if (!wait_bar(smem_u32(&ctl->kv_empty[s]), ((n / kStages) & 1) ^ 1, abort_flag, a.status)) break;
       ctl->tinfo[s] = fl | (nk <= kt_hi ? 4u : 0u);  // published by the release of the arrive below
@@ -556,7 +562,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
       __syncwarp();
     };
     uint32_t fl0;
-    const bool any = fwd_next_tile(a, b, h, qt0, gap, kt_hi, kt_lo - 1, fl0) <= kt_hi;
+    const bool any = fwd_next_tile<kFirst>(a, b, h, qt0, gap, kt_hi, kt_lo - 1, fl0) <= kt_hi;
     uint32_t info = 0;
     int npv[2] = {0, 0};
     int n = 0;
@@ -627,15 +633,15 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
     int cbase = kt_lo - 32;
     uint32_t cword = 0;
     for (int kt = kt_lo; kt <= kt_hi && ok; ++kt) {
-      if (kt == gap.lo && (kt = gap.hi) > kt_hi) break;
+      if (kFirst && kt == gap.lo && (kt = gap.hi) > kt_hi) break;
       if (kt - cbase >= 32) {
         cbase = kt;
         const int mk = kt + lane;
         cword = 0;
         if (mk <= kt_hi) {
-          cword = wg_class(a, b, h, qt, mk);
+          cword = wg_class<kFirst>(a, b, h, qt, mk);
           if (cword == kPartial)
-            cword |= ((uint32_t)lookup_class(a.ct, a.m, a.Tq, a.Tk, b, h, 2 * qt + (t >> 6), mk) & 3u) << 2;
+            cword |= ((uint32_t)lookup_class<kFirst>(a.ct, a.m, a.Tq, a.Tk, b, h, 2 * qt + (t >> 6), mk) & 3u) << 2;
         }
       }
       const uint32_t cv = __shfl_sync(0xffffffffu, cword, kt - cbase);
@@ -644,7 +650,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
       uint64_t mw0 = ~0ull, mw1 = ~0ull;
       if (cls == kPartial) {
         mw0 = mw1 = 0ull;
-        if (row < a.Tq) fwd_row_bits(a, b, h, row, (int64_t)kt * kBN, (uint8_t)(cv >> 2), mw0, mw1);
+        if (row < a.Tq) fwd_row_bits<kFirst>(a, b, h, row, (int64_t)kt * kBN, (uint8_t)(cv >> 2), mw0, mw1);
       }
       uint64_t kb0 = ~0ull, kb1 = ~0ull;
       if constexpr (kDrop) fwd_keep_bits(a.m, b, h, row, (int64_t)kt * kBN, kb0, kb1);
@@ -1502,7 +1508,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
   const int kvh = h / (f.Hq / f.Hkv);
   const int q0 = qt * kBM;
   int kt_lo, kt_hi;
-  fwd_key_tiles(f.m, b, f.Tq, f.Tk, q0, kBM, kt_lo, kt_hi);
+  fwd_key_tiles<kFirst>(f.m, b, f.Tq, f.Tk, q0, kBM, kt_lo, kt_hi);
   const FwdGap gap = kFirst ? fwd_gap(f.m, q0) : FwdGap{-1, -1};
 
   if (threadIdx.x == 0) {
@@ -1672,7 +1678,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
       uint64_t mw = ~0ull, kw = ~0ull;
       if (cls == kPartial) {
         uint64_t w0 = 0ull, w1 = 0ull;
-        if (row < f.Tq) fwd_row_bits(f, b, h, row, (int64_t)kt * kBN, (uint8_t)(cv >> 2), w0, w1);
+        if (row < f.Tq) fwd_row_bits<kFirst>(f, b, h, row, (int64_t)kt * kBN, (uint8_t)(cv >> 2), w0, w1);
         mw = w ? w1 : w0;
       }
       if (f.m.dropout) {
@@ -1983,12 +1989,12 @@ size_t bwd_split_bytes(const BwdSplit& sp, int B, int Hkv, int Tk) {
 }
 
 // Raise a kernel's dynamic shared-memory limit once per device. which names
-// the kernel instantiation, one slot each: forward 0-3 and 6-7 (first keys),
-// query-centric dQ 4-5, 20-21 (with row sums) and 22-23 (with first keys), reverse
-// 8-15, split 16-19.
+// the kernel instantiation, one slot each: forward 0-3, with first keys 6-7 and
+// 24-25 (dropout), query-centric dQ 4-5, 20-21 (with row sums) and 22-23 (with
+// first keys), reverse 8-15, split 16-19.
 cudaError_t set_smem_attr(const void* fn, uint32_t bytes, int which) {
-  static bool done[24][64] = {};
-  if (which < 0 || which >= 24) return cudaErrorInvalidValue;
+  static bool done[26][64] = {};
+  if (which < 0 || which >= 26) return cudaErrorInvalidValue;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -2100,11 +2106,15 @@ cudaError_t sm100_dense_fwd(const DenseP& p, void* o, const int64_t so[3], float
   a.lse = lse;
   a.status = status;
   const bool drop = p.m.dropout != 0;
-  const bool first = p.m.first > 0 && !drop;  // (with dropout every exponential is the hardware's anyway)
-  auto kern = first ? (f16 ? fwd_kernel<true, false, true> : fwd_kernel<false, false, true>)
-              : f16 ? (drop ? fwd_kernel<true, true, false> : fwd_kernel<true, false, false>)
-                    : (drop ? fwd_kernel<false, true, false> : fwd_kernel<false, false, false>);
-  const int which = first ? 6 + (f16 ? 1 : 0) : (f16 ? 1 : 0) + (drop ? 2 : 0);
+  const bool first = p.m.first > 0;
+  using FwdFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const FwdArgs);
+  const FwdFn table[2][2][2] = {  // [first keys][dropout][fp16]
+      {{fwd_kernel<false, false, false>, fwd_kernel<true, false, false>},
+       {fwd_kernel<false, true, false>, fwd_kernel<true, true, false>}},
+      {{fwd_kernel<false, false, true>, fwd_kernel<true, false, true>},
+       {fwd_kernel<false, true, true>, fwd_kernel<true, true, true>}}};
+  auto kern = table[first][drop][f16];
+  const int which = (first ? drop ? 22 : 6 : 0) + (drop ? 2 : 0) + (f16 ? 1 : 0);
   if ((err = set_smem_attr(reinterpret_cast<const void*>(kern), kFwdSmem, which)) != cudaSuccess) return err;
   const int nct = (p.Tq + kFwdRows - 1) / kFwdRows;
   main_kernel_begin(st);
