@@ -57,7 +57,7 @@ __device__ __forceinline__ void finish_row(float m, float l, float (&acc)[NV], f
   if (lane == 0) *lse_out = stored_lse_ln(lse_fmt, lse, m, l);
 }
 
-template <typename T, int NQ, int NV>
+template <typename T, int NQ, int NV, bool kFirst>
 __global__ void __launch_bounds__(kWarps * 32)
 dense_fwd_rows(DenseP p, T* o, int64_t so0, int64_t so1, int64_t so2, float* lse, int64_t sl0,
                int64_t sl1, int64_t sl2) {
@@ -76,11 +76,11 @@ dense_fwd_rows(DenseP p, T* o, int64_t so0, int64_t so1, int64_t so2, float* lse
 #pragma unroll
   for (int c = 0; c < NV; ++c) acc[c] = 0.f;
   float m = -INFINITY, l = 0.f;
-  int64_t lo, hi;
-  key_range(p.m, b, i, p.Tk, lo, hi);
-  for (int64_t j = lo; j <= hi; ++j) {
-    if ((j = skip_gap(p.m, i, j)) > hi) break;
-    if (!allowed(p.m, b, h, i, j)) continue;  // empty keys leave the state untouched
+  int64_t lo, mid, next, hi;
+  key_spans<kFirst>(p.m, b, i, p.Tk, lo, mid, next, hi);
+  for (int span = 0; span < (kFirst ? 2 : 1); ++span, lo = next, mid = hi)
+  for (int64_t j = lo; j <= mid; ++j) {
+    if (!allowed<kFirst>(p.m, b, h, i, j)) continue;  // empty keys leave the state untouched
     float kr[NQ];
     load_row(Kb + j * p.sk[2], p.d, lane, kr);
     const float s = dot_lanes(q, kr) * p.scale;
@@ -171,7 +171,7 @@ rows_delta(const T* o, const T* g, int64_t rows, int inner, int64_t so1, int64_t
   if (lane == 0) delta[warp] = s;
 }
 
-template <typename T, int NQ, int NV>
+template <typename T, int NQ, int NV, bool kFirst>
 __global__ void __launch_bounds__(kWarps * 32)
 dense_dq_rows(DenseP p, const T* g, int64_t sg0, int64_t sg1, int64_t sg2, const float* lse,
               int64_t sl0, int64_t sl1, int64_t sl2, const float* delta, T* dq, int64_t sd0,
@@ -193,11 +193,11 @@ dense_dq_rows(DenseP p, const T* g, int64_t sg0, int64_t sg1, int64_t sg2, const
   const float L = lse[b * sl0 + h * sl1 + (int64_t)i * sl2];
   const float dl = delta[warp];
   if (L != -INFINITY) {
-    int64_t lo, hi;
-    key_range(p.m, b, i, p.Tk, lo, hi);
-    for (int64_t j = lo; j <= hi; ++j) {
-      if ((j = skip_gap(p.m, i, j)) > hi) break;
-      if (!allowed(p.m, b, h, i, j)) continue;
+    int64_t lo, mid, next, hi;
+    key_spans<kFirst>(p.m, b, i, p.Tk, lo, mid, next, hi);
+    for (int span = 0; span < (kFirst ? 2 : 1); ++span, lo = next, mid = hi)
+    for (int64_t j = lo; j <= mid; ++j) {
+      if (!allowed<kFirst>(p.m, b, h, i, j)) continue;
       float kr[NQ], vr[NV];
       load_row(Kb + j * p.sk[2], p.d, lane, kr);
       load_row(Vb + j * p.sv[2], p.dv, lane, vr);
@@ -220,7 +220,7 @@ dense_dq_rows(DenseP p, const T* g, int64_t sg0, int64_t sg1, int64_t sg2, const
 
 // One warp per (b, kv head, key j): dK_j and dV_j summed over every query head
 // of the group and every query row that allows j, in a fixed order.
-template <typename T, int NQ, int NV>
+template <typename T, int NQ, int NV, bool kFirst>
 __global__ void __launch_bounds__(kWarps * 32)
 dense_dkv_rows(DenseP p, const T* g, int64_t sg0, int64_t sg1, int64_t sg2, const float* lse,
                int64_t sl0, int64_t sl1, int64_t sl2, const float* delta, T* dk, int64_t sdk0,
@@ -240,13 +240,13 @@ dense_dkv_rows(DenseP p, const T* g, int64_t sg0, int64_t sg1, int64_t sg2, cons
 #pragma unroll
   for (int c = 0; c < NV; ++c) av[c] = 0.f;
   int64_t lo, hi;
-  query_range(p.m, b, j, p.Tq, lo, hi);
+  query_range<kFirst>(p.m, b, j, p.Tq, lo, hi);
   for (int hh = 0; hh < group; ++hh) {
     const int h = kvh * group + hh;
     const T* Qb = static_cast<const T*>(p.q) + b * p.sq[0] + h * p.sq[1];
     const T* Gb = g + b * sg0 + h * sg1;
     for (int64_t i = lo; i <= hi; ++i) {
-      if (!allowed(p.m, b, h, i, j)) continue;
+      if (!allowed<kFirst>(p.m, b, h, i, j)) continue;
       const float L = lse[b * sl0 + h * sl1 + i * sl2];
       if (L == -INFINITY) continue;
       float q[NQ], gr[NV];
@@ -456,8 +456,10 @@ cudaError_t launch_dense_fwd_rows(const DenseP& p, void* o, const int64_t so[3],
   const int64_t rows = (int64_t)p.B * p.Hq * p.Tq;
   if (rows == 0) return cudaSuccess;
   const int w = width_class(p.d > p.dv ? p.d : p.dv);
-  ATTN_DISPATCH_WIDTH(w, dense_fwd_rows<T, NQ, NV><<<blocks_for_warps(rows), kWarps * 32, 0, st>>>(
-                             p, static_cast<T*>(o), so[0], so[1], so[2], lse, sl[0], sl[1], sl[2]);)
+  ATTN_DISPATCH_WIDTH(w,
+      auto kern = p.m.first ? dense_fwd_rows<T, NQ, NV, true> : dense_fwd_rows<T, NQ, NV, false>;
+      kern<<<blocks_for_warps(rows), kWarps * 32, 0, st>>>(p, static_cast<T*>(o), so[0], so[1], so[2], lse, sl[0],
+                                                           sl[1], sl[2]);)
   return cudaGetLastError();
 }
 
@@ -499,10 +501,12 @@ cudaError_t launch_dense_bwd_rows(const DenseP& p, const void* g, const int64_t 
   const int64_t qrows = (int64_t)p.B * p.Hq * p.Tq, krows = (int64_t)p.B * p.Hkv * p.Tk;
   if (qrows == 0) return cudaSuccess;
   ATTN_DISPATCH_WIDTH(w,
-      dense_dq_rows<T, NQ, NV><<<blocks_for_warps(qrows), kWarps * 32, 0, st>>>(
+      auto kdq = p.m.first ? dense_dq_rows<T, NQ, NV, true> : dense_dq_rows<T, NQ, NV, false>;
+      kdq<<<blocks_for_warps(qrows), kWarps * 32, 0, st>>>(
           p, static_cast<const T*>(g), sg[0], sg[1], sg[2], lse, sl[0], sl[1], sl[2], delta,
           static_cast<T*>(dq), sdq[0], sdq[1], sdq[2]);
-      dense_dkv_rows<T, NQ, NV><<<blocks_for_warps(krows), kWarps * 32, 0, st>>>(
+      auto kdkv = p.m.first ? dense_dkv_rows<T, NQ, NV, true> : dense_dkv_rows<T, NQ, NV, false>;
+      kdkv<<<blocks_for_warps(krows), kWarps * 32, 0, st>>>(
           p, static_cast<const T*>(g), sg[0], sg[1], sg[2], lse, sl[0], sl[1], sl[2], delta,
           static_cast<T*>(dk), sdk[0], sdk[1], sdk[2], static_cast<T*>(dv), sdv[0], sdv[1], sdv[2]);)
   return cudaGetLastError();
