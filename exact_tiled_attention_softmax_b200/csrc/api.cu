@@ -677,9 +677,10 @@ attn_status attn_cache_read(const attn_cache* cache, attn_tensor* k, attn_tensor
   if ((int64_t)p.batch * p.Hkv >= kMaxRowWarps / (T ? T : 1)) return ATTN_ERR_UNSUPPORTED;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if ((st = optional_status(workspace, workspace_bytes, cs, p)) != ATTN_OK) return st;
-  // Rows past what the table can hold are never written: at most 2^30 of them are looked at.
-  const int64_t cap = (int64_t)p.max_pages * p.page_size, rows = T < cap ? T : cap;
-  if (!p.batch || !rows) return ATTN_OK;
+  if (!p.batch || !T) return ATTN_OK;
+  // Rows past what the table can hold are never written and not looked at (2^30 at most;
+  // one, of a table without pages, so that the lengths are still checked).
+  const int64_t cap = (int64_t)p.max_pages * p.page_size, rows = T < cap ? T : cap ? cap : 1;
   const int64_t sok[3] = {k->stride[0], k->stride[1], k->stride[2]}, sov[3] = {v->stride[0], v->stride[1], v->stride[2]};
   return cuda_status(launch_cache_read(p, k->data, sok, v->data, sov, (int)rows, k->dtype, cs));
 }

@@ -266,6 +266,59 @@ def test_rows_outside_every_sequence_and_strides(kind, new, cd):
     check(o2, lse2, *ref, tensor_core=True, cache=cd)
 
 
+@pytest.mark.parametrize("cd", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [64, 100, 128, 160, 256, 300])
+def test_many_query_heads_over_one(group, cd):
+    """Row blocks of two tokens, of one, of a token that fills them, and a group
+    wider than a block; one new token and several."""
+    new, lens = [1, 3, 5], [200, 3, 131]
+    cache, K, V = make_cache(lens, 16, 1, 128, 128, DT[cd], seed=33, src=torch.bfloat16)
+    q = seeded_q(sum(new), group, 128, torch.bfloat16, 34)
+    mask = dict(causal=True, window=50, first=3)
+    o, lse = run(q, cache, new, allowed=allowed_of(mask), max_q=max(new))
+    check(o, lse, *reference(q, K, V, new, lens, 128 ** -0.5, **mask), tensor_core=True, cache=cd)
+
+
+@pytest.mark.parametrize("max_q", [0, 1, 100])
+def test_calls_with_nothing_to_do(max_q):
+    """No tokens, no sequences, tables without pages, pools without pages."""
+    a = eta.AllowedSet(causal=True)
+    dt = torch.bfloat16
+    cache, _, _ = make_cache([40, 20], 16, 2, 128, 128, dt, seed=2)
+    q = seeded_q(4, 4, 128, dt)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    # no tokens: with cu_q and without
+    for cu in (None, cu_of([0, 0])):
+        o, lse = eta.attn_paged_fwd(q[:0], cache, cu, a, max_q=max_q)
+        assert o.shape == (0, 4, 128) and lse.shape == (0, 4)
+        eta.attn_cache_write(q[:0, :2], q[:0, :2], cache, cu, workspace=ws)
+        assert eta.attn_get_status(ws) == 0
+    # rows that belong to nobody: cu_q all zero, and no sequence at all
+    none = eta.PagedCache(cache.k, cache.v, cache.block_table[:0], cache.seq_lens[:0])
+    before = bits(cache.k)
+    for c, cu in ((cache, cu_of([0, 0])), (none, cu_of([]))):
+        o = torch.full((4, 4, 128), 3.0, dtype=dt, device="cuda")
+        lse = torch.full((4, 4), 3.0, device="cuda")
+        big = torch.full((eta.attn_paged_workspace_size(q, c, a),), 255, dtype=torch.uint8, device="cuda")
+        eta.attn_paged_fwd(q, c, cu, a, max_q=max_q, out=o, lse=lse, workspace=big)
+        assert eta.attn_get_status(big) == 0 and (o == 3).all() and (lse == 3).all()
+        eta.attn_cache_write(q[:, :2], q[:, :2], c, cu, workspace=ws)
+        assert eta.attn_get_status(ws) == 0
+    assert torch.equal(bits(cache.k), before)
+    assert eta.attn_cache_read(none, 5)[0].shape == (0, 2, 5, 128)
+    # tables without pages: every length is past the table, every row empty
+    flat = eta.PagedCache(cache.k, cache.v, cache.block_table[:, :0].contiguous(), cache.seq_lens)
+    o, lse = run(q, flat, [2, 2], allowed=a, max_q=max_q, status=eta.ATTN_DEVERR_RAGGED)
+    assert (o == 0).all() and (lse == -math.inf).all()
+    assert eta.attn_cache_read(flat, 0)[0].shape == (2, 2, 0, 128) and eta.attn_cache_read(flat)[0].shape[2] == 0
+    assert (eta.attn_cache_read(flat, 7, workspace=ws)[0] == 0).all()
+    assert eta.attn_get_status(ws) == eta.ATTN_DEVERR_RAGGED
+    # a pool without pages: every page number is outside it
+    bare = eta.PagedCache(cache.k[:0], cache.v[:0], cache.block_table, cache.seq_lens)
+    o, lse = run(q, bare, [2, 2], allowed=a, max_q=max_q, status=eta.ATTN_DEVERR_PAGE)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
 @pytest.mark.parametrize("fmt", [(True, False), (False, True), (True, True)])
 @pytest.mark.parametrize("kind", ["decode", "chunk", "page_7"])
 def test_lse_formats(kind, fmt):
